@@ -32,7 +32,11 @@ from ._lib import (MOE_DEV_TIMEOUT, MOE_EPI_BF16, MOE_EPI_F32, MOE_EPI_SWIGLU_QU
                    moe_router_backward_workspace_size,
                    moe_dx_combine, moe_wgrad_max_blocks, moe_wgrad_layout, moe_wgrad_quant_x,
                    moe_wgrad_quant_do, moe_wgrad_quant_h, moe_wgrad_quant_dac,
-                   moe_grouped_gemm_wgrad)
+                   moe_grouped_gemm_wgrad, MOE_T_BF16, MOE_T_CKPT, MOE_T_F16, MOE_T_F32,
+                   moe_layernorm_forward, moe_layernorm_backward,
+                   moe_layernorm_backward_workspace_size, moe_ckpt_row_bytes, moe_ckpt_pack,
+                   moe_ckpt_unpack, moe_swiglu_backward_quant_ckpt, moe_wgrad_quant_h_ckpt,
+                   moe_wgrad_quant_dac_ckpt, moe_gate_backward_ckpt)
 
 __all__ = ["MoeLayer", "MoeShape", "MoeError", "lib", "make_shape", "moe_version"]
 

@@ -19,6 +19,10 @@ MOE_EPI_F32 = 0
 MOE_EPI_BF16 = 1
 MOE_EPI_SWIGLU_QUANT = 2
 MOE_DEV_TIMEOUT = 1
+MOE_T_F32 = 0
+MOE_T_BF16 = 1
+MOE_T_F16 = 2
+MOE_T_CKPT = 3
 
 
 class MoeError(RuntimeError):
@@ -111,6 +115,16 @@ def lib() -> ctypes.CDLL:
             "moe_layer_mx_workspace_size": (SZ, [SP]),
             "moe_layer_forward_mx": (I, [SP, ctypes.POINTER(MoeWeightsMx), P, P, P,
                                          ctypes.POINTER(MoeRouting), P, I, P, SZ, P, P]),
+            "moe_layernorm_forward": (I, [P, I, I64, I, P, P, ctypes.c_float, P, P, P, P, P]),
+            "moe_layernorm_backward_workspace_size": (SZ, [I64, I]),
+            "moe_layernorm_backward": (I, [P, I, P, I, P, I64, I, P, P, P, P, P, P, P, SZ, P, P]),
+            "moe_ckpt_row_bytes": (I64, [I64]),
+            "moe_ckpt_pack": (I, [P, I, I64, I64, P, P, P, P]),
+            "moe_ckpt_unpack": (I, [P, P, I64, I64, P, I, P, P]),
+            "moe_swiglu_backward_quant_ckpt": (I, [P, P, P, I64, I, I64, P, P, P, P]),
+            "moe_wgrad_quant_h_ckpt": (I, [P, P, I64, I, P, I, P, P, P, P]),
+            "moe_wgrad_quant_dac_ckpt": (I, [P, P, P, I64, I, P, I, P, P, P, P]),
+            "moe_gate_backward_ckpt": (I, [SP, P, P, P, P, P, P, P, P, P]),
             "moe_split_groups": (I, [SP, P, P, P, P, I, P, P, P, P]),
             "moe_combine": (I, [SP, P, P, P, P, P, P, P]),
             "moe_update_bias": (I, [SP, P, P, P, P]),
@@ -547,3 +561,154 @@ def moe_grouped_gemm_wgrad(n_groups, kb_offsets, nkb_total, a_t, a_scales, m, b_
     _check("moe_grouped_gemm_wgrad", lib().moe_grouped_gemm_wgrad(
         int(n_groups), _ptr(kb_offsets), int(nkb_total), _ptr(a_t), _ptr(a_scales), int(m),
         _ptr(b_t), _ptr(b_scales), int(n), _ptr(out), _ptr(dev_status), _stream(stream)))
+
+
+# --------------------------------- layer norm, 8-bit checkpoints, dense block
+_TYPES = {}
+
+
+def _type(t, name, kept=False) -> int:
+    """Type code of a tensor; uint8 is a checkpoint's codes where `kept`."""
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.float32: MOE_T_F32, torch.bfloat16: MOE_T_BF16,
+                       torch.float16: MOE_T_F16, torch.uint8: MOE_T_CKPT})
+    code = _TYPES.get(t.dtype)
+    if code is None or (code == MOE_T_CKPT and not kept):
+        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+    return code
+
+
+def _mat(name, t, shape, dtype=None):
+    """Checks one tensor argument (None passes): on the current CUDA device,
+    contiguous, of this shape (and dtype): the library sees only its address."""
+    if t is None:
+        return
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: needs a tensor on the current CUDA device, got {t.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+
+
+def _tiles(n) -> int:
+    return (n + 127) // 128
+
+
+def _wide(n) -> int:
+    return (n + 127) // 128 * 128
+
+
+def moe_layernorm_forward(x, weight, bias, eps, y, mean=None, rstd=None, dev_status=None,
+                          stream=None):
+    """y = layer norm of x [rows, cols]; weight, bias fp32 [cols] or None;
+    mean, rstd fp32 [rows] out or None."""
+    import torch
+    f32 = torch.float32
+    ty = _type(x, "x")
+    rows, cols = x.shape
+    _mat("x", x, (rows, cols))
+    _mat("y", y, (rows, cols), x.dtype)
+    _mat("weight", weight, (cols,), f32)
+    _mat("bias", bias, (cols,), f32)
+    _mat("mean", mean, (rows,), f32)
+    _mat("rstd", rstd, (rows,), f32)
+    _check("moe_layernorm_forward", lib().moe_layernorm_forward(
+        _ptr(x), ty, rows, cols, _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(mean),
+        _ptr(rstd), _ptr(dev_status), _stream(stream)))
+
+
+def moe_layernorm_backward_workspace_size(rows, cols) -> int:
+    return int(lib().moe_layernorm_backward_workspace_size(int(rows), int(cols)))
+
+
+def moe_layernorm_backward(dy, x, x_scales, weight, mean, rstd, dx, dweight, dbias, ws,
+                           dev_status=None, stream=None):
+    """Gradients of moe_layernorm_forward.  x as the forward pass had it
+    (x_scales None), or kept in 8 bits (uint8 codes and their x_scales)."""
+    import torch
+    f32 = torch.float32
+    ty, xt = _type(dy, "dy"), _type(x, "x", kept=True)
+    rows, cols = dy.shape
+    kept = xt == MOE_T_CKPT
+    _mat("dy", dy, (rows, cols))
+    _mat("x", x, (rows, _wide(cols) if kept else cols))
+    if kept == (x_scales is None):
+        raise ValueError("x_scales goes with x kept in 8 bits")
+    _mat("x_scales", x_scales, (_tiles(cols), rows), f32)
+    _mat("weight", weight, (cols,), f32)
+    _mat("mean", mean, (rows,), f32)
+    _mat("rstd", rstd, (rows,), f32)
+    _mat("dx", dx, (rows, cols), dy.dtype)
+    _mat("dweight", dweight, (cols,), f32)
+    _mat("dbias", dbias, (cols,), f32)
+    nbytes = ws.numel() * ws.element_size() if ws is not None else 0
+    _check("moe_layernorm_backward", lib().moe_layernorm_backward(
+        _ptr(dy), ty, _ptr(x), xt, _ptr(x_scales), rows, cols, _ptr(weight), _ptr(mean),
+        _ptr(rstd), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, _ptr(dev_status),
+        _stream(stream)))
+
+
+def moe_ckpt_row_bytes(cols) -> int:
+    return int(lib().moe_ckpt_row_bytes(int(cols)))
+
+
+def moe_ckpt_pack(x, q, scales, dev_status=None, stream=None):
+    """x [rows, cols] -> q uint8 [rows, moe_ckpt_row_bytes(cols)], scales fp32
+    [ceil(cols / 128), rows]."""
+    import torch
+    ty = _type(x, "x")
+    rows, cols = x.shape
+    _mat("x", x, (rows, cols))
+    _mat("q", q, (rows, _wide(cols)), torch.uint8)
+    _mat("scales", scales, (_tiles(cols), rows), torch.float32)
+    _check("moe_ckpt_pack", lib().moe_ckpt_pack(_ptr(x), ty, rows, cols, _ptr(q), _ptr(scales),
+                                                _ptr(dev_status), _stream(stream)))
+
+
+def moe_ckpt_unpack(q, scales, y, dev_status=None, stream=None):
+    """The kept values as y [rows, cols] (its dtype)."""
+    import torch
+    ty = _type(y, "y")
+    rows, cols = y.shape
+    _mat("y", y, (rows, cols))
+    _mat("q", q, (rows, _wide(cols)), torch.uint8)
+    _mat("scales", scales, (_tiles(cols), rows), torch.float32)
+    _check("moe_ckpt_unpack", lib().moe_ckpt_unpack(_ptr(q), _ptr(scales), rows, cols, _ptr(y), ty,
+                                                    _ptr(dev_status), _stream(stream)))
+
+
+def moe_swiglu_backward_quant_ckpt(dh, ac_q, ac_scales, rows, inter, rows_total, q, q_scales,
+                                   dev_status=None, stream=None):
+    """moe_swiglu_backward_quant from [a | c] kept in 8 bits."""
+    _check("moe_swiglu_backward_quant_ckpt", lib().moe_swiglu_backward_quant_ckpt(
+        _ptr(dh), _ptr(ac_q), _ptr(ac_scales), int(rows), int(inter), int(rows_total), _ptr(q),
+        _ptr(q_scales), _ptr(dev_status), _stream(stream)))
+
+
+def moe_wgrad_quant_h_ckpt(ac_q, ac_scales, inter, blocks, ht, ht_scales, dev_status=None,
+                           stream=None):
+    """moe_wgrad_quant_h from [a | c] kept in 8 bits."""
+    _check("moe_wgrad_quant_h_ckpt", lib().moe_wgrad_quant_h_ckpt(
+        _ptr(ac_q), _ptr(ac_scales), int(ac_scales.shape[1]), int(inter), _ptr(blocks),
+        int(blocks.shape[0]), _ptr(ht), _ptr(ht_scales), _ptr(dev_status), _stream(stream)))
+
+
+def moe_wgrad_quant_dac_ckpt(dh, ac_q, ac_scales, inter, blocks, dact, dact_scales,
+                             dev_status=None, stream=None):
+    """moe_wgrad_quant_dac from [a | c] kept in 8 bits."""
+    _check("moe_wgrad_quant_dac_ckpt", lib().moe_wgrad_quant_dac_ckpt(
+        _ptr(dh), _ptr(ac_q), _ptr(ac_scales), int(ac_scales.shape[1]), int(inter), _ptr(blocks),
+        int(blocks.shape[0]), _ptr(dact), _ptr(dact_scales), _ptr(dev_status), _stream(stream)))
+
+
+def moe_gate_backward_ckpt(shape, dy, o_q, o_scales, row_of_pair, topk_score, dgate, du,
+                           dev_status=None, stream=None):
+    """moe_gate_backward from expert outputs kept in 8 bits."""
+    _check("moe_gate_backward_ckpt", lib().moe_gate_backward_ckpt(
+        ctypes.byref(shape), _ptr(dy), _ptr(o_q), _ptr(o_scales), _ptr(row_of_pair),
+        _ptr(topk_score), _ptr(dgate), _ptr(du), _ptr(dev_status), _stream(stream)))

@@ -26,7 +26,7 @@
 // values (the transposed-GEMM need the pages raise in their discussion).
 #include <algorithm>
 
-#include "common.cuh"
+#include "elem.cuh"
 
 namespace moe {
 namespace {
@@ -188,34 +188,64 @@ __global__ void __launch_bounds__(256) swiglu_backward_quant_kernel(
 // each of the KM rows, all in flight together) and keeps KM FP64 partial
 // sums; one shuffle tree per slot at the end.  Then the chosen scores'
 // gradients in FP64.
-template <int KM>
+// OT: float, or e4m3_t for outputs kept in 8 bits: the warp's 128 columns of
+// a step are one tile, whose scale multiplies the lane's four exact products'
+// sum once.
+template <class OT, int KM>
 __global__ void __launch_bounds__(256) gate_backward_kernel(
-    const uint16_t* __restrict__ dy, const float* __restrict__ o, int T, int d, int K,
+    const uint16_t* __restrict__ dy, const OT* __restrict__ o,
+    const float* __restrict__ o_scales, int64_t o_rows, int T, int d, int K,
     const int32_t* __restrict__ row_of_pair, const float* __restrict__ score,
     float* __restrict__ dgate, float* __restrict__ du) {
+    constexpr bool KEPT = sizeof(OT) == 1;
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
     if (t >= T) return;
-    const float4* rows[KM];
+    const OT* rows[KM];
+    int row_at[KM];  // KEPT: the row's index in o_scales
     double acc[KM];
 #pragma unroll
     for (int k = 0; k < KM; ++k) {
         const int row = k < K ? row_of_pair[int64_t(t) * K + k] : -1;
-        rows[k] = row >= 0 ? reinterpret_cast<const float4*>(o + int64_t(row) * d) : nullptr;
+        rows[k] = row >= 0 ? o + int64_t(row) * d : nullptr;
+        row_at[k] = row;
         acc[k] = 0.0;
     }
     const uint2* dyr = reinterpret_cast<const uint2*>(dy + int64_t(t) * d);
     for (int c = lane; c < d / 4; c += 32) {
         const uint2 w = __ldg(dyr + c);
         const double y0 = bf16_lo(w.x), y1 = bf16_hi(w.x), y2 = bf16_lo(w.y), y3 = bf16_hi(w.y);
-        float4 v[KM];
+        if constexpr (KEPT) {
+            uint32_t q[KM];
+            float sc[KM];
 #pragma unroll
-        for (int k = 0; k < KM; ++k)
-            v[k] = rows[k] ? __ldg(rows[k] + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < KM; ++k) {
+                q[k] = 0u;
+                sc[k] = 0.0f;
+                if (rows[k]) {
+                    q[k] = __ldg(reinterpret_cast<const uint32_t*>(rows[k]) + c);
+                    sc[k] = __ldg(o_scales + int64_t(c / 32) * o_rows + row_at[k]);
+                }
+            }
 #pragma unroll
-        for (int k = 0; k < KM; ++k)
-            acc[k] += y0 * double(v[k].x) + y1 * double(v[k].y) + y2 * double(v[k].z) +
-                      y3 * double(v[k].w);
+            for (int k = 0; k < KM; ++k) {
+                // a bf16 value times a code is exact in fp32, their sums FP64
+                const float2 lo = e4m3x2_to_float2(uint16_t(q[k] & 0xFFFFu));
+                const float2 hi = e4m3x2_to_float2(uint16_t(q[k] >> 16));
+                acc[k] += double(sc[k]) * (y0 * double(lo.x) + y1 * double(lo.y) +
+                                           y2 * double(hi.x) + y3 * double(hi.y));
+            }
+        } else {
+            float4 v[KM];
+#pragma unroll
+            for (int k = 0; k < KM; ++k)
+                v[k] = rows[k] ? __ldg(reinterpret_cast<const float4*>(rows[k]) + c)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < KM; ++k)
+                acc[k] += y0 * double(v[k].x) + y1 * double(v[k].y) + y2 * double(v[k].z) +
+                          y3 * double(v[k].w);
+        }
     }
     double my_dg = 0.0;
 #pragma unroll
@@ -483,7 +513,8 @@ __global__ void __launch_bounds__(1024) wgrad_layout_kernel(
     for (int b = total + t; b < max_blocks; b += blockDim.x) blocks[b] = make_int2(0, 0);
 }
 
-enum WgSource { kWgX = 0, kWgDo = 1, kWgH = 2, kWgDac = 3 };
+// kWgHKept, kWgDacKept: the same from [a | c] kept in 8 bits
+enum WgSource { kWgX = 0, kWgDo = 1, kWgH = 2, kWgDac = 3, kWgHKept = 4, kWgDacKept = 5 };
 
 struct WgSrc {
     const uint16_t* x;          // x or dy, bf16 [T, d]
@@ -492,7 +523,24 @@ struct WgSrc {
     const float* dh;            // [rows, I]
     const float* ac;            // [rows, 2I]
     int T, K, I;
+    const uint8_t* ac_q;        // [rows, 2I] codes
+    const float* ac_scales;     // [2I/128, rows_total]
+    int64_t rows_total;
 };
+
+// Two neighbouring values of a row of [a | c] (column col): fp32, or codes
+// times their tile's scale.
+template <bool KEPT>
+__device__ __forceinline__ float2 wg_ac(const WgSrc& s, int64_t row, int col) {
+    if constexpr (KEPT) {
+        const uint16_t q = __ldg(reinterpret_cast<const uint16_t*>(s.ac_q + row * 2 * s.I + col));
+        const float sc = __ldg(s.ac_scales + int64_t(col / kTile) * s.rows_total + row);
+        const float2 v = e4m3x2_to_float2(q);
+        return make_float2(v.x * sc, v.y * sc);
+    } else {
+        return __ldg(reinterpret_cast<const float2*>(s.ac + row * 2 * s.I + col));
+    }
+}
 
 // token of a permutation row and the gate its gradient carries
 __device__ __forceinline__ int wg_token(const WgSrc& s, int r, float& g) {
@@ -570,16 +618,15 @@ __global__ void __launch_bounds__(256) wgrad_quant_kernel(
                         v1[i] = __fmul_rn(g[i], v1[i]);
                     }
                 }
-            } else if (SRC == kWgH) {
+            } else if (SRC == kWgH || SRC == kWgHKept) {
                 float2 a[8], c[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int rr = warp + 8 * (i0 + i);
                     a[i] = c[i] = make_float2(0.f, 0.f);
                     if (rr < blk.y) {
-                        const float* ar = src.ac + int64_t(blk.x + rr) * 2 * src.I;
-                        a[i] = __ldg(reinterpret_cast<const float2*>(ar + fl));
-                        c[i] = __ldg(reinterpret_cast<const float2*>(ar + src.I + fl));
+                        a[i] = wg_ac<SRC == kWgHKept>(src, blk.x + rr, fl);
+                        c[i] = wg_ac<SRC == kWgHKept>(src, blk.x + rr, src.I + fl);
                     }
                 }
 #pragma unroll
@@ -597,10 +644,9 @@ __global__ void __launch_bounds__(256) wgrad_quant_kernel(
                     h[i] = a[i] = c[i] = make_float2(0.f, 0.f);
                     if (rr < blk.y) {
                         const int64_t r = blk.x + rr;
-                        const float* ar = src.ac + r * 2 * src.I;
                         h[i] = __ldg(reinterpret_cast<const float2*>(src.dh + r * src.I + j));
-                        a[i] = __ldg(reinterpret_cast<const float2*>(ar + j));
-                        if (is_da) c[i] = __ldg(reinterpret_cast<const float2*>(ar + src.I + j));
+                        a[i] = wg_ac<SRC == kWgDacKept>(src, r, j);
+                        if (is_da) c[i] = wg_ac<SRC == kWgDacKept>(src, r, src.I + j);
                     }
                 }
 #pragma unroll
@@ -664,6 +710,27 @@ RouterBwdWs router_bwd_ws(const MoeShape& s) {
     w.partial = w.blocks + up(sizeof(int32_t) * 2 * size_t(w.n_blocks));
     w.total = w.partial + up(sizeof(float) * size_t(w.n_blocks) * s.d);
     return w;
+}
+
+template <class OT>
+int launch_gate_backward(const MoeShape* s, const uint16_t* dy, const OT* o, const float* o_scales,
+                         const int32_t* row_of_pair, const float* score, float* dgate, float* du,
+                         cudaStream_t st) {
+    const int T = s->T, K = s->topk, grid = (T + 7) / 8;
+    const int64_t R = int64_t(T) * K + T;
+    if (K <= 4)
+        gate_backward_kernel<OT, 4><<<grid, 256, 0, st>>>(dy, o, o_scales, R, T, s->d, K,
+                                                          row_of_pair, score, dgate, du);
+    else if (K <= 8)
+        gate_backward_kernel<OT, 8><<<grid, 256, 0, st>>>(dy, o, o_scales, R, T, s->d, K,
+                                                          row_of_pair, score, dgate, du);
+    else if (K <= 16)
+        gate_backward_kernel<OT, 16><<<grid, 256, 0, st>>>(dy, o, o_scales, R, T, s->d, K,
+                                                           row_of_pair, score, dgate, du);
+    else
+        gate_backward_kernel<OT, 32><<<grid, 256, 0, st>>>(dy, o, o_scales, R, T, s->d, K,
+                                                           row_of_pair, score, dgate, du);
+    return check_launch();
 }
 
 int pieces_per(int n, int& PC) {
@@ -753,22 +820,25 @@ extern "C" MOE_API int moe_gate_backward(const MoeShape* shape, const uint16_t* 
     const int T = shape->T;
     if (T == 0) return MOE_OK;
     if (!dy || !expert_out || !row_of_pair || !topk_score || !dgate || !du) return MOE_ERR_NULL;
-    const int K = shape->topk, grid = (T + 7) / 8;
-    cudaStream_t st = as_stream(stream);
     if (!aligned16(expert_out) || (reinterpret_cast<uintptr_t>(dy) & 7)) return MOE_ERR_ALIGN;
-    if (K <= 4)
-        gate_backward_kernel<4><<<grid, 256, 0, st>>>(dy, expert_out, T, shape->d, K, row_of_pair,
-                                                      topk_score, dgate, du);
-    else if (K <= 8)
-        gate_backward_kernel<8><<<grid, 256, 0, st>>>(dy, expert_out, T, shape->d, K, row_of_pair,
-                                                      topk_score, dgate, du);
-    else if (K <= 16)
-        gate_backward_kernel<16><<<grid, 256, 0, st>>>(dy, expert_out, T, shape->d, K,
-                                                       row_of_pair, topk_score, dgate, du);
-    else
-        gate_backward_kernel<32><<<grid, 256, 0, st>>>(dy, expert_out, T, shape->d, K,
-                                                       row_of_pair, topk_score, dgate, du);
-    return check_launch();
+    return launch_gate_backward<float>(shape, dy, expert_out, nullptr, row_of_pair, topk_score,
+                                       dgate, du, as_stream(stream));
+}
+
+extern "C" MOE_API int moe_gate_backward_ckpt(const MoeShape* shape, const uint16_t* dy,
+                                              const uint8_t* o_q, const float* o_scales,
+                                              const int32_t* row_of_pair, const float* topk_score,
+                                              float* dgate, float* du, int* dev_status,
+                                              void* stream) {
+    (void)dev_status;
+    int rc = validate_shape(shape);
+    if (rc != MOE_OK) return rc;
+    if (shape->T == 0) return MOE_OK;
+    if (!dy || !o_q || !o_scales || !row_of_pair || !topk_score || !dgate || !du)
+        return MOE_ERR_NULL;
+    if (!aligned16(o_q) || (reinterpret_cast<uintptr_t>(dy) & 7)) return MOE_ERR_ALIGN;
+    return launch_gate_backward<e4m3_t>(shape, dy, reinterpret_cast<const e4m3_t*>(o_q), o_scales,
+                                        row_of_pair, topk_score, dgate, du, as_stream(stream));
 }
 
 extern "C" MOE_API int moe_router_backward(const MoeShape* shape, const uint16_t* x,
@@ -916,4 +986,30 @@ extern "C" MOE_API int moe_wgrad_quant_dac(const float* dh, const float* ac, int
     if (n_blocks > 0 && (!dh || !ac)) return MOE_ERR_NULL;
     WgSrc s{nullptr, nullptr, nullptr, dh, ac, 0, 1, inter};
     return launch_wgrad_quant<kWgDac>(s, blocks, n_blocks, 2 * inter, dact, dact_scales, stream);
+}
+
+extern "C" MOE_API int moe_wgrad_quant_h_ckpt(const uint8_t* ac_q, const float* ac_scales,
+                                              int64_t rows_total, int inter,
+                                              const int32_t* blocks, int n_blocks, uint8_t* ht,
+                                              float* ht_scales, int* dev_status, void* stream) {
+    (void)dev_status;
+    if (inter <= 0 || inter % 128 || rows_total < 0) return MOE_ERR_SHAPE;
+    if (n_blocks > 0 && (!ac_q || !ac_scales)) return MOE_ERR_NULL;
+    if (!aligned16(ac_q)) return MOE_ERR_ALIGN;
+    WgSrc s{nullptr, nullptr, nullptr, nullptr, nullptr, 0, 1, inter, ac_q, ac_scales, rows_total};
+    return launch_wgrad_quant<kWgHKept>(s, blocks, n_blocks, inter, ht, ht_scales, stream);
+}
+
+extern "C" MOE_API int moe_wgrad_quant_dac_ckpt(const float* dh, const uint8_t* ac_q,
+                                                const float* ac_scales, int64_t rows_total,
+                                                int inter, const int32_t* blocks, int n_blocks,
+                                                uint8_t* dact, float* dact_scales,
+                                                int* dev_status, void* stream) {
+    (void)dev_status;
+    if (inter <= 0 || inter % 128 || rows_total < 0) return MOE_ERR_SHAPE;
+    if (n_blocks > 0 && (!dh || !ac_q || !ac_scales)) return MOE_ERR_NULL;
+    if (!aligned16(ac_q)) return MOE_ERR_ALIGN;
+    WgSrc s{nullptr, nullptr, nullptr, dh, nullptr, 0, 1, inter, ac_q, ac_scales, rows_total};
+    return launch_wgrad_quant<kWgDacKept>(s, blocks, n_blocks, 2 * inter, dact, dact_scales,
+                                          stream);
 }

@@ -734,6 +734,105 @@ MOE_API int moe_grouped_gemm_wgrad(int n_groups, const int32_t* kb_offsets, int 
                                    const uint8_t* b_t, const float* b_scales, int n, float* out,
                                    int* dev_status, void* stream);
 
+/* ====================================================================
+ * Next to the layer: its normalisation, 8-bit activation checkpoints, and
+ * the dense gated block of the layers that have no experts.
+ *
+ * Element types of the entry points below (`type` arguments).  Matrices are
+ * contiguous, row-major. */
+#define MOE_T_F32 0
+#define MOE_T_BF16 1
+#define MOE_T_F16 2
+#define MOE_T_CKPT 3   /* E4M3 codes of an 8-bit checkpoint, with scales */
+
+/* ----------------------------------------------------------- layer norm
+ * moe_layernorm_forward: per row, mu = mean(x), rstd = 1 / sqrt(mean((x -
+ * mu)^2) + eps), y = (x - mu) rstd weight + bias.  Statistics in fp32 (the
+ * variance from the centred values), one rounding to y's type.
+ *   x, y         [rows, cols] of `type` (MOE_T_F32, _BF16 or _F16); y may be x
+ *   weight, bias fp32 [cols]; NULL: ones, zeros
+ *   mean, rstd   fp32 [rows] out; NULL: not kept
+ * cols in 1..16384, any value; pointers aligned to their element.  Rows of
+ * whole 16-byte pieces (cols % 8 == 0, 16-byte aligned pointers) are the
+ * fast form.  rows == 0 does nothing.
+ *
+ * moe_layernorm_backward: with xh = (x - mean) rstd and g = dy weight,
+ *   dx = rstd (g - mean(g) - xh mean(g xh)),
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy.
+ *   dy, dx       [rows, cols] of `type`; dx may be dy
+ *   x            [rows, cols] of `x_type`: `type`, a 16-bit type when `type`
+ *                is MOE_T_F32, or MOE_T_CKPT: codes and x_scales of
+ *                moe_ckpt_pack (x 16-byte aligned); x_scales NULL otherwise
+ *   mean, rstd   as the forward pass left them
+ *   dweight, dbias fp32 [cols] out, or NULL; every sum is fp32 and taken in
+ *                an order fixed by rows and the device (the same call gives
+ *                the same bits).  rows == 0 gives zeros
+ *   ws           scratch of moe_layernorm_backward_workspace_size(rows, cols)
+ *                bytes, 16-byte aligned; not read when dweight and dbias are
+ *                both NULL.  Calls in flight together need their own.
+ * Errors: MOE_ERR_ARG (types, eps < 0), MOE_ERR_SHAPE, MOE_ERR_NULL,
+ * MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE, MOE_ERR_CUDA. */
+MOE_API int moe_layernorm_forward(const void* x, int type, int64_t rows, int cols,
+                                  const float* weight, const float* bias, float eps, void* y,
+                                  float* mean, float* rstd, int* dev_status, void* stream);
+MOE_API size_t moe_layernorm_backward_workspace_size(int64_t rows, int cols);
+MOE_API int moe_layernorm_backward(const void* dy, int type, const void* x, int x_type,
+                                   const float* x_scales, int64_t rows, int cols,
+                                   const float* weight, const float* mean, const float* rstd,
+                                   void* dx, float* dweight, float* dbias, void* ws,
+                                   size_t ws_bytes, int* dev_status, void* stream);
+
+/* -------------------------------------------------- 8-bit checkpoints
+ * A matrix kept between the forward and the backward pass in E4M3, one fp32
+ * scale per 1x128 tile of a row ("FP8 mixed precision training": activations
+ * kept in FP8 for the backward pass): scale = fp32(amax / 448), code =
+ * E4M3(fp32(v * inverse)) with inverse = fp32(448 * fp32(1 / amax)); a tile
+ * of zeros has scale 1.  (The scale rule at the top of this file with the
+ * inverse rounded twice: codes differ only next to a border.)  A tile that holds an infinity comes back as NaN; a NaN comes back
+ * as NaN and leaves the other values of its tile alone.
+ *   q       uint8 [rows, moe_ckpt_row_bytes(cols)], 16-byte aligned; the
+ *           bytes past the last column of a row are written as zeros
+ *   scales  fp32 [ceil(cols / 128), rows]
+ *
+ * moe_ckpt_row_bytes: cols rounded up to a multiple of 128 (-1 when cols is
+ *   negative or above 2^31 - 1).
+ * moe_ckpt_pack: x [rows, cols] of `type` (MOE_T_F32, _BF16, _F16) -> q,
+ *   scales.  Any cols; x aligned to its element, fast for cols % 8 == 0 and
+ *   16-byte aligned x.
+ * moe_ckpt_unpack: y = type(fp32(code scale)).
+ *
+ * The backward steps that read a checkpoint where it lies:
+ * moe_swiglu_backward_quant_ckpt: moe_swiglu_backward_quant with [a | c] kept
+ *   as ac_q (uint8 [rows, 2 inter]) and ac_scales (fp32 [2 inter / 128,
+ *   rows_total]).
+ * moe_wgrad_quant_h_ckpt, moe_wgrad_quant_dac_ckpt: moe_wgrad_quant_h and
+ *   _dac with [a | c] kept so; rows_total is the scales' row length.
+ * moe_gate_backward_ckpt: moe_gate_backward with the expert outputs kept as
+ *   o_q (uint8 [R, d]) and o_scales (fp32 [d / 128, R]), R = T K + T.
+ * Errors: MOE_ERR_ARG, MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_ALIGN,
+ * MOE_ERR_DEVICE, MOE_ERR_CUDA. */
+MOE_API int64_t moe_ckpt_row_bytes(int64_t cols);
+MOE_API int moe_ckpt_pack(const void* x, int type, int64_t rows, int64_t cols, uint8_t* q,
+                          float* scales, int* dev_status, void* stream);
+MOE_API int moe_ckpt_unpack(const uint8_t* q, const float* scales, int64_t rows, int64_t cols,
+                            void* y, int type, int* dev_status, void* stream);
+MOE_API int moe_swiglu_backward_quant_ckpt(const float* dh, const uint8_t* ac_q,
+                                           const float* ac_scales, int64_t rows, int inter,
+                                           int64_t rows_total, uint8_t* q, float* q_scales,
+                                           int* dev_status, void* stream);
+MOE_API int moe_wgrad_quant_h_ckpt(const uint8_t* ac_q, const float* ac_scales,
+                                   int64_t rows_total, int inter, const int32_t* blocks,
+                                   int n_blocks, uint8_t* ht, float* ht_scales, int* dev_status,
+                                   void* stream);
+MOE_API int moe_wgrad_quant_dac_ckpt(const float* dh, const uint8_t* ac_q,
+                                     const float* ac_scales, int64_t rows_total, int inter,
+                                     const int32_t* blocks, int n_blocks, uint8_t* dact,
+                                     float* dact_scales, int* dev_status, void* stream);
+MOE_API int moe_gate_backward_ckpt(const MoeShape* shape, const uint16_t* dy, const uint8_t* o_q,
+                                   const float* o_scales, const int32_t* row_of_pair,
+                                   const float* topk_score, float* dgate, float* du,
+                                   int* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
