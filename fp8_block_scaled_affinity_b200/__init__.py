@@ -36,7 +36,8 @@ from ._lib import (MOE_DEV_TIMEOUT, MOE_EPI_BF16, MOE_EPI_F32, MOE_EPI_SWIGLU_QU
                    moe_layernorm_forward, moe_layernorm_backward,
                    moe_layernorm_backward_workspace_size, moe_ckpt_row_bytes, moe_ckpt_pack,
                    moe_ckpt_unpack, moe_swiglu_backward_quant_ckpt, moe_wgrad_quant_h_ckpt,
-                   moe_wgrad_quant_dac_ckpt, moe_gate_backward_ckpt)
+                   moe_wgrad_quant_dac_ckpt, moe_gate_backward_ckpt, moe_ffn_forward,
+                   moe_ffn_backward)
 
 __all__ = ["MoeLayer", "MoeShape", "MoeError", "lib", "make_shape", "moe_version"]
 

@@ -125,6 +125,8 @@ def lib() -> ctypes.CDLL:
             "moe_wgrad_quant_h_ckpt": (I, [P, P, I64, I, P, I, P, P, P, P]),
             "moe_wgrad_quant_dac_ckpt": (I, [P, P, P, I64, I, P, I, P, P, P, P]),
             "moe_gate_backward_ckpt": (I, [SP, P, P, P, P, P, P, P, P, P]),
+            "moe_ffn_forward": (I, [P, P, P, I, I64, I, I, P, P, P, I, P, P, P]),
+            "moe_ffn_backward": (I, [P, P, P, P, P, I, P, I, I64, I, I, P, P, P, P, P, P, P]),
             "moe_split_groups": (I, [SP, P, P, P, P, I, P, P, P, P]),
             "moe_combine": (I, [SP, P, P, P, P, P, P, P]),
             "moe_update_bias": (I, [SP, P, P, P, P]),
@@ -712,3 +714,61 @@ def moe_gate_backward_ckpt(shape, dy, o_q, o_scales, row_of_pair, topk_score, dg
     _check("moe_gate_backward_ckpt", lib().moe_gate_backward_ckpt(
         ctypes.byref(shape), _ptr(dy), _ptr(o_q), _ptr(o_scales), _ptr(row_of_pair),
         _ptr(topk_score), _ptr(dgate), _ptr(du), _ptr(dev_status), _stream(stream)))
+
+
+def _kept_ac(ac, ac_scales, dtype, T, inter) -> int:
+    """Checks a and c kept by moe_ffn_forward; their type code."""
+    import torch
+    if ac is None:
+        if ac_scales is not None:
+            raise ValueError("ac_scales goes with ac in 8 bits")
+        return MOE_T_CKPT
+    kept = ac.dtype == torch.uint8
+    if kept == (ac_scales is None):
+        raise ValueError("ac_scales goes with ac in 8 bits")
+    w = _wide(inter) if kept else inter
+    _mat("ac", ac, (T, 2 * w), torch.uint8 if kept else dtype)
+    _mat("ac_scales", ac_scales, (2 * _tiles(inter), T), torch.float32)
+    return _type(ac, "ac", kept=True)
+
+
+def moe_ffn_forward(x, w13, w2, h, y, ac=None, ac_scales=None, dev_status=None, stream=None):
+    """y = (silu(x W1^T) (x W3^T)) W2^T for x [T, d], w13 [2 inter, d], w2
+    [d, inter]; h [T, inter] out; ac, ac_scales: a and c kept for
+    moe_ffn_backward, in 8 bits (uint8 and scales) or in x's type."""
+    T, d = x.shape
+    inter = w2.shape[1]
+    ty = _type(x, "x")
+    _mat("x", x, (T, d))
+    _mat("w13", w13, (2 * inter, d), x.dtype)
+    _mat("w2", w2, (d, inter), x.dtype)
+    _mat("h", h, (T, inter), x.dtype)
+    _mat("y", y, (T, d), x.dtype)
+    at = _kept_ac(ac, ac_scales, x.dtype, T, inter)
+    _check("moe_ffn_forward", lib().moe_ffn_forward(
+        _ptr(x), _ptr(w13), _ptr(w2), ty, T, d, inter, _ptr(h), _ptr(y), _ptr(ac), at,
+        _ptr(ac_scales), _ptr(dev_status), _stream(stream)))
+
+
+def moe_ffn_backward(dy, x, w13, w2, ac, ac_scales, dac, h, dx=None, dw13=None, dw2=None,
+                     dev_status=None, stream=None):
+    """Gradients of moe_ffn_forward from the kept a and c; dac [T, 2 inter]
+    and h [T, inter] are written on the way; dx, dw13, dw2 may be None."""
+    T, d = dy.shape
+    inter = w2.shape[1]
+    ty = _type(dy, "dy")
+    _mat("dy", dy, (T, d))
+    _mat("x", x, (T, d), dy.dtype)
+    _mat("w13", w13, (2 * inter, d), dy.dtype)
+    _mat("w2", w2, (d, inter), dy.dtype)
+    if ac is None:
+        raise ValueError("moe_ffn_backward needs the kept ac")
+    at = _kept_ac(ac, ac_scales, dy.dtype, T, inter)
+    _mat("dac", dac, (T, 2 * inter), dy.dtype)
+    _mat("h", h, (T, inter), dy.dtype)
+    _mat("dx", dx, (T, d), dy.dtype)
+    _mat("dw13", dw13, (2 * inter, d), dy.dtype)
+    _mat("dw2", dw2, (d, inter), dy.dtype)
+    _check("moe_ffn_backward", lib().moe_ffn_backward(
+        _ptr(dy), _ptr(x), _ptr(w13), _ptr(w2), _ptr(ac), at, _ptr(ac_scales), ty, T, d, inter,
+        _ptr(dac), _ptr(h), _ptr(dx), _ptr(dw13), _ptr(dw2), _ptr(dev_status), _stream(stream)))

@@ -1,0 +1,735 @@
+// Dense gated feed-forward block in 16 bits (bf16 or fp16), forward and
+// backward, on tcgen05.
+//
+//   a = x W1^T, c = x W3^T, h = silu(a) c, y = h W2^T
+//   dh = dy W2, s = sigmoid(a), da = dh c s (1 + a (1 - s)), dc = dh a s
+//   dx = da W1 + dc W3, dW13 = [da | dc]^T x, dW2 = dy^T h
+//
+// Every product runs through one kernel: CTA pairs (cta_group::2) of 256 x
+// (up to 256) output tiles, 64 K elements a stage, six stages fed by TMA,
+// the fp32 accumulator in TMEM twice, so that a tile's epilogue runs under
+// the next tile's products.  An operand whose K runs along its rows in
+// memory (W2 and W13 in the backward pass, all operands of the weight
+// gradients) is read as it lies, as an MN-major tile: nothing is transposed
+// in memory.  The epilogues are the element-wise steps:
+//   kGated     a and c of the same 128 features lie in one tile (one CTA of
+//              the pair loads 128 rows of W1, the other 128 of W3): h, and
+//              where asked a and c kept for the backward pass, in 8 bits
+//              (1x128 tiles) or in 16;
+//   kBackward  dh stays in TMEM: da, dc and h from it and the kept a, c;
+//   kPlain     the product.
+// dx, dW13 and dW2 do not depend on one another and are one launch over one
+// list of tiles, so that the last round of tiles is left part empty once and
+// not three times.
+//
+// Accumulators are fp32.  h and [da | dc] are rounded to the operands' type
+// between two products (the tensor cores take 16-bit operands); everything
+// else is rounded once, on output.  Bound by the tensor cores for hundreds of
+// tokens and more.
+#include <cuda.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "elem.cuh"
+#include "tc_pair.cuh"
+
+namespace moe {
+
+// 2D map over [rows, cols] with a row pitch in bytes, any element type and
+// box (defined with the grouped GEMM).
+bool make_map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t rows,
+                 uint64_t cols, uint64_t pitch_bytes, uint32_t box_rows,
+                 uint32_t box_cols, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promote);
+
+namespace {
+
+using namespace tc;
+
+enum Epilogue { kPlain = 0, kGated = 1, kBackward = 2 };
+enum Kept { kKeptNone = 0, kKept8 = 1, kKept16 = 2 };
+
+constexpr int kThreads = 384;
+constexpr int kStages = 6;
+constexpr int kTileM = 256;               // rows of a pair's tile, 128 a CTA
+constexpr int kTileK = 64;                // K elements of a stage
+constexpr int kOperandBytes = 128 * 128;  // 128 rows of 64 16-bit elements
+constexpr int kPieceBytes = 64 * 128;     // MN-major piece: 64 K x 64 elements
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kEpiWarps = 8;
+constexpr int kChunk = 32;                // output columns of one epilogue step
+constexpr int kBoxBytes = 32 * 64;        // 32 rows x 32 16-bit elements
+constexpr int kMaxProblems = 3;
+constexpr int kGroupM = 8;                // row tiles walked together
+
+struct Problem {
+    CUtensorMap a, b, out;
+    int m, n;                // output rows and columns
+    int nkb;                 // stages of K
+    int nt;                  // tile columns (multiple of 32, at most 256)
+    int tiles_m, tiles_n;
+    int first;               // index of its first tile in the launch's list
+    int a_mn, b_mn;          // operand's K runs along its rows in memory
+};
+
+struct Args {
+    Problem p[kMaxProblems];
+    CUtensorMap o1, o2;      // kGated 16-bit a, c; kBackward dc, h
+    int n_problems;
+    int tiles;
+    int inter;
+    int64_t rows;            // tokens
+    void* ac;                // kept a, c
+    float* ac_scales;
+    int* dev_status;
+    uint64_t wait_limit_ns;
+};
+
+struct Shared {
+    uint64_t full[kStages];
+    uint64_t empty[kStages];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t drain;
+    PairState ps;
+    uint32_t tmem_base;
+};
+
+template <int EPI>
+struct Cfg {
+    static constexpr int kBoxes = EPI == kGated ? 1 : 2;  // parked boxes per epilogue warp
+    static constexpr int kParkBytes = kEpiWarps * kBoxes * kBoxBytes;
+    // kGated: amax of a and c, [tile parity][column half][a, c][row]
+    static constexpr int kRedBytes = EPI == kGated ? 2 * 2 * 2 * 128 * 4 : 0;
+    static constexpr size_t kSmem =
+        size_t(kStages) * kStageBytes + kParkBytes + kRedBytes + sizeof(Shared) + 1024;
+};
+static_assert(Cfg<kPlain>::kSmem <= 232448 && Cfg<kGated>::kSmem <= 232448 &&
+                  Cfg<kBackward>::kSmem <= 232448,
+              "dynamic shared memory above the sm_100 limit per CTA");
+
+struct Tile {
+    int p;       // problem
+    int m0, n0;  // first row; first column (kGated: first feature)
+};
+
+// Tiles of a problem in groups of kGroupM row tiles, rows fastest: the tiles
+// that run side by side share few operand tiles, which stay in L2.
+__device__ __forceinline__ Tile decode(const Args& a, int t, int col_step) {
+    Tile r;
+    r.p = 0;
+    while (r.p + 1 < a.n_problems && t >= a.p[r.p + 1].first) ++r.p;
+    const Problem& p = a.p[r.p];
+    t -= p.first;
+    const int per_group = kGroupM * p.tiles_n;
+    const int g = t / per_group;
+    const int in_g = t - g * per_group;
+    const int gm = min(kGroupM, p.tiles_m - g * kGroupM);
+    r.m0 = (g * kGroupM + in_g % gm) * kTileM;
+    r.n0 = (in_g / gm) * (col_step ? col_step : p.nt);
+    return r;
+}
+
+template <int EPI>
+__device__ __forceinline__ Tile decode_for(const Args& a, int t) {
+    return decode(a, t, EPI == kGated ? 128 : 0);
+}
+
+// ------------------------------------------------ TMA producer (warp 0)
+template <int EPI>
+__device__ __forceinline__ void producer(const Args& a, uint8_t* smem, Shared* ss, int rank,
+                                         int unit, int units) {
+    if ((threadIdx.x & 31) == 0) {
+        uint32_t it = 0, issued = 0, issued_parity = 0;
+        bool ok = true;
+        for (int t = unit; ok && t < a.tiles; t += units) {
+            const Tile w = decode_for<EPI>(a, t);
+            const Problem& p = a.p[w.p];
+            const int half = p.nt / 2;
+            const int am = w.m0 + 128 * rank;
+            // this CTA's rows of B: half the tile's columns, or 128 rows of
+            // W1 (rank 0) and of W3 (rank 1)
+            const int bn = EPI == kGated ? w.n0 + rank * a.inter : w.n0 + rank * half;
+            const int b_pieces = (half + 63) / 64;
+            const uint32_t b_bytes = p.b_mn ? b_pieces * kPieceBytes : half * 128;
+            const uint32_t tx = 2 * (kOperandBytes + b_bytes);
+            for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+                const int s = it % kStages;
+                const uint32_t par = (it / kStages) & 1u;
+                ok = pair_wait(smem_u32(&ss->empty[s]), par ^ 1u, &ss->ps, a.dev_status);
+                if (!ok) break;
+                const uint32_t sa = smem_u32(smem + size_t(s) * kStageBytes);
+                const uint32_t sb = sa + kOperandBytes;
+                const uint32_t local = smem_u32(&ss->full[s]);
+                const uint32_t bar = mapa(local, 0);
+                const int k0 = kb * kTileK;
+                if (rank == 0) mbar_arrive_expect_tx(local, tx);
+                if (p.a_mn) {
+                    pair_tma_load_2d(sa, &p.a, bar, am, k0);
+                    pair_tma_load_2d(sa + kPieceBytes, &p.a, bar, am + 64, k0);
+                } else {
+                    pair_tma_load_2d(sa, &p.a, bar, k0, am);
+                }
+                if (p.b_mn) {
+                    for (int i = 0; i < b_pieces; ++i)
+                        pair_tma_load_2d(sb + i * kPieceBytes, &p.b, bar, bn + 64 * i, k0);
+                } else {
+                    pair_tma_load_2d(sb, &p.b, bar, k0, bn);
+                }
+                issued |= 1u << s;
+                issued_parity = (issued_parity & ~(1u << s)) | (par << s);
+            }
+        }
+        if (!ok && rank == 0)  // loads in flight land before the CTA leaves
+            for (int s = 0; s < kStages; ++s)
+                if ((issued >> s) & 1u)
+                    mbar_quiesce(smem_u32(&ss->full[s]), (issued_parity >> s) & 1u, nullptr,
+                                 ss->ps.wait_limit);
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------ MMA issuer (warp 1 of the leader)
+template <int EPI, bool BF16>
+__device__ __forceinline__ void issuer(const Args& a, uint8_t* smem, Shared* ss,
+                                       uint32_t tmem_base, int unit, int units) {
+    if ((threadIdx.x & 31) == 0) {
+        uint32_t it = 0, n = 0;
+        bool ok = true;
+        for (int t = unit; ok && t < a.tiles; t += units, ++n) {
+            const Tile w = decode_for<EPI>(a, t);
+            const Problem& p = a.p[w.p];
+            const uint32_t idesc = idesc_f16(BF16, p.a_mn, p.b_mn, kTileM, p.nt);
+            // bytes per 16 K elements, in descriptor units of 16
+            const uint32_t a_step = p.a_mn ? 2048 / 16 : 32 / 16;
+            const uint32_t b_step = p.b_mn ? 2048 / 16 : 32 / 16;
+            const uint32_t d = tmem_base + (n & 1) * 256;
+            ok = pair_wait(smem_u32(&ss->tempty[n & 1]), ((n >> 1) & 1u) ^ 1u, &ss->ps,
+                           a.dev_status);
+            if (!ok) break;
+            fence_after();
+            for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+                const int s = it % kStages;
+                ok = pair_wait(smem_u32(&ss->full[s]), (it / kStages) & 1u, &ss->ps,
+                               a.dev_status);
+                if (!ok) break;
+                fence_after();
+                const uint32_t sa = smem_u32(smem + size_t(s) * kStageBytes);
+                uint64_t ad = sw128_desc16(sa, kPieceBytes);
+                uint64_t bd = sw128_desc16(sa + kOperandBytes, kPieceBytes);
+#pragma unroll
+                for (int kk = 0; kk < kTileK / 16; ++kk) {
+                    pair_mma_f16(d, ad, bd, idesc, (kb | kk) ? 1u : 0u);
+                    ad += a_step;
+                    bd += b_step;
+                }
+                pair_commit_both(smem_u32(&ss->empty[s]));
+            }
+            if (ok) pair_commit_both(smem_u32(&ss->tfull[n & 1]));
+        }
+        // every MMA has completed once this fires (after an abort too)
+        pair_commit(smem_u32(&ss->drain));
+        mbar_quiesce(smem_u32(&ss->drain), 0, nullptr, ss->ps.wait_limit);
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------ epilogue (warps 4-11)
+// One 32-column step of a warp's 32 rows: rounded to T, parked in the 64-byte
+// swizzle of the output map (16-byte piece j of row r at j ^ (r / 2 % 4)) and
+// handed to the TMA engine, which clips rows and columns past the end.
+template <class T, int BOXES>
+__device__ __forceinline__ void put32(const float (&v)[32], char* park, int& box,
+                                      const CUtensorMap* map, int x, int y, bool any) {
+    const int lane = threadIdx.x & 31;
+    char* const b = park + box * kBoxBytes;
+    box = box + 1 == BOXES ? 0 : box + 1;
+    if (lane == 0) bulk_wait_read<BOXES - 1>();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(b + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) = make_uint4(
+            pack2t(T(), v[8 * j], v[8 * j + 1]), pack2t(T(), v[8 * j + 2], v[8 * j + 3]),
+            pack2t(T(), v[8 * j + 4], v[8 * j + 5]), pack2t(T(), v[8 * j + 6], v[8 * j + 7]));
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (any) tma_store_2d(map, smem_u32(b), x, y);
+        bulk_commit();
+    }
+}
+
+// sigmoid from the fast exponential and reciprocal (about 1e-6 relative;
+// e^-a = inf gives 0)
+__device__ __forceinline__ float sigmoid_fast(float a) {
+    return __fdividef(1.0f, 1.0f + __expf(-a));
+}
+
+// 32 values -> 32 codes at q (32-byte aligned)
+__device__ __forceinline__ void put_codes(uint8_t* q, const float (&v)[32], float inv) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float* f = v + 16 * j + 4 * i;
+            w[i] = e4m3x2(__fmul_rn(f[0], inv), __fmul_rn(f[1], inv)) |
+                   (uint32_t(e4m3x2(__fmul_rn(f[2], inv), __fmul_rn(f[3], inv))) << 16);
+        }
+        reinterpret_cast<uint4*>(q)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// A step's kept a and c of one row, as they lie in memory.
+template <int KEPT>
+struct KeptRaw {
+    uint4 a[KEPT == kKept8 ? 2 : 4], c[KEPT == kKept8 ? 2 : 4];
+    float sa, sc;
+};
+template <int KEPT>
+__device__ __forceinline__ KeptRaw<KEPT> load_kept(const Args& a, int64_t row, int f) {
+    KeptRaw<KEPT> k;
+    memset(&k, 0, sizeof(k));
+    if (row < a.rows && f < a.inter) {
+        if constexpr (KEPT == kKept8) {
+            const int64_t wide = (a.inter + kTile - 1) / kTile * kTile;
+            const uint8_t* q = static_cast<const uint8_t*>(a.ac) + row * 2 * wide + f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                k.a[j] = __ldg(reinterpret_cast<const uint4*>(q) + j);
+                k.c[j] = __ldg(reinterpret_cast<const uint4*>(q + wide) + j);
+            }
+            k.sa = __ldg(a.ac_scales + int64_t(f / kTile) * a.rows + row);
+            k.sc = __ldg(a.ac_scales + (wide / kTile + f / kTile) * a.rows + row);
+        } else {
+            const uint16_t* q = static_cast<const uint16_t*>(a.ac) + row * 2 * a.inter + f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (f + 8 * j < a.inter) {
+                    k.a[j] = __ldg(reinterpret_cast<const uint4*>(q) + j);
+                    k.c[j] = __ldg(reinterpret_cast<const uint4*>(q + a.inter) + j);
+                }
+        }
+    }
+    return k;
+}
+// Values 8 j .. 8 j + 7 of a step.
+template <class T, int KEPT>
+__device__ __forceinline__ void kept_floats(const uint4* q, int j, float s, float (&f)[8]) {
+    if constexpr (KEPT == kKept8) {
+        const uint4 w = q[j / 2];
+        Raw<e4m3_t, 8> r;
+        r.a = j & 1 ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y);
+        raw_floats(r, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= s;
+    } else {
+        Raw<T, 8> r;
+        r.a = q[j];
+        raw_floats(r, f);
+    }
+}
+
+template <int EPI, int KEPT, class T>
+__device__ __forceinline__ void epilogue(const Args& a, Shared* ss, char* park_area, float* red,
+                                         uint32_t tmem_base, int rank, int unit, int units) {
+    constexpr int BOXES = Cfg<EPI>::kBoxes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lane_addr = tmem_base + (uint32_t(q * 32) << 16);
+    char* const park = park_area + (warp - 4) * (BOXES * kBoxBytes);
+    int box = 0;
+    uint32_t n = 0;
+    for (int t = unit; t < a.tiles; t += units, ++n) {
+        const Tile w = decode_for<EPI>(a, t);
+        const Problem& p = a.p[w.p];
+        const int y0 = w.m0 + 128 * rank + 32 * q;
+        const int64_t row = y0 + lane;
+        const bool rows_any = y0 < p.m;
+        constexpr int RAW = KEPT == kKept16 ? kKept16 : kKept8;
+        KeptRaw<RAW> kept;
+        if constexpr (EPI == kBackward) kept = load_kept<RAW>(a, row, w.n0 + kChunk * half);
+        bool ok = true;
+        if (lane == 0)
+            ok = pair_wait(smem_u32(&ss->tfull[n & 1]), (n >> 1) & 1u, &ss->ps, a.dev_status);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        // all epilogue warps agree on whether to go on
+        if (named_bar_or(2, kEpiWarps * 32,
+                         !ok || *reinterpret_cast<volatile int*>(&ss->ps.abort_flag)))
+            break;
+        fence_after();
+        const uint32_t tm = lane_addr + (n & 1) * 256;
+        if constexpr (EPI == kPlain) {
+            for (int ch = half; ch < p.nt / kChunk; ch += 2) {
+                uint32_t v[32];
+                tmem_ld32(tm + ch * kChunk, v);
+                float f[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+                const int x = w.n0 + ch * kChunk;
+                put32<T, BOXES>(f, park, box, &p.out, x, y0, rows_any && x < p.n);
+            }
+        } else if constexpr (EPI == kGated) {
+            float ia = 1.0f, ic = 1.0f;
+            const int64_t wide = (a.inter + kTile - 1) / kTile * kTile;
+            if constexpr (KEPT == kKept8) {
+                // a first look at the tile for the 1x128 scales of a and c;
+                // each warp sees 64 of the 128 features, its partner the rest
+                float ma = 0.0f, mc = 0.0f;
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    const int col = 64 * half + kChunk * ch;
+                    uint32_t va[32], vc[32];
+                    tmem_ld32(tm + col, va);
+                    tmem_ld32(tm + 128 + col, vc);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (w.n0 + col + (i & ~7) < a.inter) {  // 8 features exist together
+                            ma = fmaxf(ma, fabsf(__uint_as_float(va[i])));
+                            mc = fmaxf(mc, fabsf(__uint_as_float(vc[i])));
+                        }
+                }
+                float* const r = red + (n & 1) * 512 + q * 32 + lane;
+                r[half * 256] = ma;
+                r[half * 256 + 128] = mc;
+                named_bar(1, kEpiWarps * 32);
+                ma = fmaxf(ma, r[(half ^ 1) * 256]);
+                mc = fmaxf(mc, r[(half ^ 1) * 256 + 128]);
+                float sa, sc;
+                kept_scale(ma, sa, ia);
+                kept_scale(mc, sc, ic);
+                if (half == 0 && row < a.rows) {
+                    a.ac_scales[int64_t(w.n0 / kTile) * a.rows + row] = sa;
+                    a.ac_scales[(wide / kTile + w.n0 / kTile) * a.rows + row] = sc;
+                }
+            }
+#pragma unroll 1
+            for (int ch = 0; ch < 2; ++ch) {
+                const int col = 64 * half + kChunk * ch;
+                const int x = w.n0 + col;
+                uint32_t va[32], vc[32];
+                tmem_ld32(tm + col, va);
+                tmem_ld32(tm + 128 + col, vc);
+                float fa[32], fc[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    fa[i] = __uint_as_float(va[i]);
+                    fc[i] = __uint_as_float(vc[i]);
+                }
+                if constexpr (KEPT == kKept8) {
+                    if (row < a.rows) {
+                        // columns past the last feature (rows of W3 for a) are kept as zeros
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (x + (i & ~7) >= a.inter) fa[i] = fc[i] = 0.0f;
+                        uint8_t* o = static_cast<uint8_t*>(a.ac) + row * 2 * wide + x;
+                        put_codes(o, fa, ia);
+                        put_codes(o + wide, fc, ic);
+                    }
+                } else if constexpr (KEPT == kKept16) {
+                    put32<T, BOXES>(fa, park, box, &a.o1, x, y0, rows_any && x < a.inter);
+                    put32<T, BOXES>(fc, park, box, &a.o2, x, y0, rows_any && x < a.inter);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) fa[i] = fa[i] * sigmoid_fast(fa[i]) * fc[i];
+                put32<T, BOXES>(fa, park, box, &p.out, x, y0, rows_any && x < a.inter);
+            }
+        } else {
+            for (int ch = half; ch < p.nt / kChunk; ch += 2) {
+                const int x = w.n0 + ch * kChunk;
+                uint32_t v[32];
+                tmem_ld32(tm + ch * kChunk, v);
+                const int after = ch + 2 < p.nt / kChunk ? x + 2 * kChunk : a.inter;
+                const KeptRaw<RAW> next = load_kept<RAW>(a, row, after);
+                float da[32], dc[32], h[32];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float ka[8], kc[8];
+                    kept_floats<T, KEPT>(kept.a, j, kept.sa, ka);
+                    kept_floats<T, KEPT>(kept.c, j, kept.sc, kc);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float dh = __uint_as_float(v[8 * j + i]);
+                        const float s = sigmoid_fast(ka[i]);
+                        const float as = ka[i] * s, ds = dh * s;
+                        h[8 * j + i] = as * kc[i];
+                        dc[8 * j + i] = dh * as;
+                        da[8 * j + i] = ds * kc[i] * fmaf(ka[i], 1.0f - s, 1.0f);
+                    }
+                }
+                const bool any = rows_any && x < a.inter;
+                put32<T, BOXES>(da, park, box, &p.out, x, y0, any);
+                put32<T, BOXES>(dc, park, box, &a.o1, x, y0, any);
+                put32<T, BOXES>(h, park, box, &a.o2, x, y0, any);
+                kept = next;
+            }
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&ss->tempty[n & 1]), 0));
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+    fence_before();
+}
+
+template <int EPI, int KEPT, class T>
+__global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant__ Args a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    char* park = reinterpret_cast<char*>(smem + kStages * kStageBytes);
+    float* red = reinterpret_cast<float*>(park + Cfg<EPI>::kParkBytes);
+    Shared* ss = reinterpret_cast<Shared*>(park + Cfg<EPI>::kParkBytes + Cfg<EPI>::kRedBytes);
+    const int warp = threadIdx.x >> 5;
+    const int rank = int(cluster_rank());
+    const int unit = int(blockIdx.x >> 1), units = int(gridDim.x >> 1);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&ss->full[s]), 1);
+            mbar_init(smem_u32(&ss->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&ss->tfull[b]), 1);
+            mbar_init(smem_u32(&ss->tempty[b]), 2 * kEpiWarps);
+        }
+        mbar_init(smem_u32(&ss->drain), 1);
+        ss->ps.wait_limit = a.wait_limit_ns;
+        ss->ps.abort_flag = 0;
+        ss->ps.peer_abort = mapa(smem_u32(&ss->ps.abort_flag), uint32_t(rank ^ 1));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) pair_tmem_alloc(smem_u32(&ss->tmem_base));
+    fence_before();
+    __syncthreads();
+    cluster_sync();  // the peer's barriers exist before anyone signals them
+    fence_after();
+    const uint32_t tmem_base = ss->tmem_base;
+    if (warp == 0)
+        producer<EPI>(a, smem, ss, rank, unit, units);
+    else if (warp == 1 && rank == 0)
+        issuer<EPI, std::is_same<T, bf16_t>::value>(a, smem, ss, tmem_base, unit, units);
+    else if (warp >= 4)
+        epilogue<EPI, KEPT, T>(a, ss, park, red, tmem_base, rank, unit, units);
+    __syncthreads();
+    // neither CTA leaves while the other may still signal its barriers or
+    // the leader's MMAs may still read its shared memory
+    cluster_sync();
+    if (warp == 1) {
+        fence_after();
+        pair_tmem_free(tmem_base);
+    }
+}
+
+// -------------------------------------------------------------------- host
+// CTA pairs the device holds at once (cached per device).
+template <int EPI, int KEPT, class T>
+int pair_units(cudaLaunchConfig_t& cfg) {
+    static int cache[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (cudaFuncSetAttribute(ffn_kernel<EPI, KEPT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(Cfg<EPI>::kSmem)) != cudaSuccess)
+        return 0;
+    if (cache[dev] == 0) {
+        int n = 0;
+        cfg.gridDim = dim3(unsigned(2 * (sm_count() / 2)), 1, 1);
+        if (cudaOccupancyMaxActiveClusters(&n, ffn_kernel<EPI, KEPT, T>, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return 0;
+        }
+        cache[dev] = std::min(n, sm_count() / 2);
+    }
+    return cache[dev];
+}
+
+template <int EPI, int KEPT, class T>
+int launch(Args& a, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Cfg<EPI>::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int units = pair_units<EPI, KEPT, T>(cfg);
+    if (units < 1) return MOE_ERR_CUDA;
+    cfg.gridDim = dim3(unsigned(2 * std::min(units, a.tiles)), 1, 1);
+    if (cudaLaunchKernelEx(&cfg, ffn_kernel<EPI, KEPT, T>, a) != cudaSuccess) return MOE_ERR_CUDA;
+    return check_launch();
+}
+
+struct Maker {
+    CUtensorMapDataType type;
+    bool ok = true;
+    // operand: K-major box of `rows` rows x 64 K, or MN-major box of 64 K
+    // rows x 64 elements
+    void operand(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows) {
+        ok = ok && make_map_2d(m, type, base, uint64_t(rows), uint64_t(cols),
+                               uint64_t(cols) * 2, uint32_t(box_rows), 64,
+                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    }
+    // output: boxes of 32 rows x 32 columns of a [rows, cols] part of rows
+    // `pitch` elements long
+    void output(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t pitch) {
+        ok = ok && make_map_2d(m, type, base, uint64_t(rows), uint64_t(cols),
+                               uint64_t(pitch) * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
+                               CU_TENSOR_MAP_L2_PROMOTION_NONE);
+    }
+};
+
+// out [m, n] = A B^T over k: A is [m, k] in memory, or [k, m] (a_mn); B is
+// [n, k], or [k, n] (b_mn).
+void product(Args& a, Maker& mk, const void* A, bool a_mn, const void* B, bool b_mn, void* out,
+             int64_t m, int64_t n, int64_t k, int nt) {
+    Problem& p = a.p[a.n_problems++];
+    p.m = int(m);
+    p.n = int(n);
+    p.nkb = int((k + kTileK - 1) / kTileK);
+    p.nt = nt;
+    p.tiles_m = int((m + kTileM - 1) / kTileM);
+    p.tiles_n = int((n + nt - 1) / nt);
+    p.first = a.tiles;
+    p.a_mn = a_mn;
+    p.b_mn = b_mn;
+    a.tiles += p.tiles_m * p.tiles_n;
+    if (a_mn) mk.operand(&p.a, A, k, m, 64);
+    else mk.operand(&p.a, A, m, k, 128);
+    if (b_mn) mk.operand(&p.b, B, k, n, 64);
+    else mk.operand(&p.b, B, n, k, nt / 2);
+    mk.output(&p.out, out, m, n, n);
+}
+
+Args make_args(int64_t T, int inter, int* dev_status) {
+    Args a = {};
+    a.rows = T;
+    a.inter = inter;
+    a.dev_status = dev_status;
+    a.wait_limit_ns = wait_limit_ns();
+    return a;
+}
+
+template <class T>
+int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t rows, int d, int I,
+            void* h, void* y, void* ac, int kept, float* ac_scales, int* dev_status,
+            cudaStream_t st) {
+    Args a = make_args(rows, I, dev_status);
+    product(a, mk, x, false, w13, false, h, rows, 2 * int64_t(I), d, 256);
+    // the gated tile: 128 features of W1 and of W3
+    Problem& p = a.p[0];
+    p.n = I;
+    p.tiles_n = (I + 127) / 128;
+    a.tiles = p.tiles_m * p.tiles_n;
+    mk.output(&p.out, h, rows, I, I);
+    a.ac = ac;
+    a.ac_scales = ac_scales;
+    if (kept == kKept16) {
+        mk.output(&a.o1, ac, rows, I, 2 * int64_t(I));
+        mk.output(&a.o2, static_cast<uint16_t*>(ac) + I, rows, I, 2 * int64_t(I));
+    }
+    Args b = make_args(rows, I, dev_status);
+    product(b, mk, h, false, w2, false, y, rows, d, I, 256);
+    if (!mk.ok) return MOE_ERR_CUDA;
+    const int rc = kept == kKept8    ? launch<kGated, kKept8, T>(a, st)
+                   : kept == kKept16 ? launch<kGated, kKept16, T>(a, st)
+                                     : launch<kGated, kKeptNone, T>(a, st);
+    return rc != MOE_OK ? rc : launch<kPlain, kKeptNone, T>(b, st);
+}
+
+template <class T>
+int backward(Maker mk, const void* dy, const void* x, const void* w13, const void* w2, void* ac,
+             int kept, const float* ac_scales, int64_t rows, int d, int I, void* dac, void* h,
+             void* dx, void* dw13, void* dw2, int* dev_status, cudaStream_t st) {
+    Args a = make_args(rows, I, dev_status);
+    a.ac = ac;
+    a.ac_scales = const_cast<float*>(ac_scales);
+    product(a, mk, dy, false, w2, true, h, rows, I, d, 256);
+    mk.output(&a.p[0].out, dac, rows, I, 2 * int64_t(I));
+    mk.output(&a.o1, static_cast<uint16_t*>(dac) + I, rows, I, 2 * int64_t(I));
+    mk.output(&a.o2, h, rows, I, I);
+    Args b = make_args(rows, I, dev_status);
+    if (dx) product(b, mk, dac, false, w13, true, dx, rows, d, 2 * int64_t(I), 256);
+    if (dw13) product(b, mk, dac, true, x, true, dw13, 2 * int64_t(I), d, rows, 256);
+    if (dw2) product(b, mk, dy, true, h, true, dw2, d, I, rows, 256);
+    if (!mk.ok) return MOE_ERR_CUDA;
+    const int rc = kept == kKept8 ? launch<kBackward, kKept8, T>(a, st)
+                                  : launch<kBackward, kKept16, T>(a, st);
+    return rc != MOE_OK || b.n_problems == 0 ? rc : launch<kPlain, kKeptNone, T>(b, st);
+}
+
+int check_sizes(int type, int64_t T, int d, int inter) {
+    if (type != MOE_T_BF16 && type != MOE_T_F16) return MOE_ERR_ARG;
+    if (T < 0 || T > (1 << 24) || d < 8 || d % 8 || inter < 8 || inter % 8 || d > (1 << 20) ||
+        inter > (1 << 20))
+        return MOE_ERR_SHAPE;
+    // 2^30 output tiles of 256 x 128 are more than any of these sizes gives
+    return MOE_OK;
+}
+
+Maker maker(int type) {
+    return Maker{type == MOE_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16};
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" MOE_API int moe_ffn_forward(const void* x, const void* w13, const void* w2, int type,
+                                       int64_t T, int d, int inter, void* h, void* y, void* ac,
+                                       int ac_type, float* ac_scales, int* dev_status,
+                                       void* stream) {
+    int rc = check_sizes(type, T, d, inter);
+    if (rc != MOE_OK) return rc;
+    if (ac && ac_type != MOE_T_CKPT && ac_type != type) return MOE_ERR_ARG;
+    if (T == 0) return MOE_OK;
+    if (!x || !w13 || !w2 || !h || !y) return MOE_ERR_NULL;
+    const int kept = !ac ? kKeptNone : ac_type == MOE_T_CKPT ? kKept8 : kKept16;
+    if (kept == kKept8 && !ac_scales) return MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(h) || !aligned16(y) ||
+        !aligned16(ac))
+        return MOE_ERR_ALIGN;
+    if (!device_is_sm100()) return MOE_ERR_DEVICE;
+    cudaStream_t st = as_stream(stream);
+    return type == MOE_T_BF16
+               ? forward<bf16_t>(maker(type), x, w13, w2, T, d, inter, h, y, ac, kept, ac_scales,
+                                 dev_status, st)
+               : forward<f16_t>(maker(type), x, w13, w2, T, d, inter, h, y, ac, kept, ac_scales,
+                                dev_status, st);
+}
+
+extern "C" MOE_API int moe_ffn_backward(const void* dy, const void* x, const void* w13,
+                                        const void* w2, const void* ac, int ac_type,
+                                        const float* ac_scales, int type, int64_t T, int d,
+                                        int inter, void* dac, void* h, void* dx, void* dw13,
+                                        void* dw2, int* dev_status, void* stream) {
+    int rc = check_sizes(type, T, d, inter);
+    if (rc != MOE_OK) return rc;
+    if (ac_type != MOE_T_CKPT && ac_type != type) return MOE_ERR_ARG;
+    cudaStream_t st = as_stream(stream);
+    if (T == 0) {
+        // no tokens: the weights' gradients are empty sums
+        const size_t n = size_t(d) * size_t(inter) * 2;
+        if ((dw13 && cudaMemsetAsync(dw13, 0, 2 * n, st) != cudaSuccess) ||
+            (dw2 && cudaMemsetAsync(dw2, 0, n, st) != cudaSuccess))
+            return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    if (!dy || !w2 || !ac || !dac || !h || (dx && !w13) || (dw13 && !x)) return MOE_ERR_NULL;
+    const int kept = ac_type == MOE_T_CKPT ? kKept8 : kKept16;
+    if (kept == kKept8 && !ac_scales) return MOE_ERR_NULL;
+    const void* all[] = {dy, x, w13, w2, ac, dac, h, dx, dw13, dw2};
+    for (const void* p : all)
+        if (!aligned16(p)) return MOE_ERR_ALIGN;
+    if (!device_is_sm100()) return MOE_ERR_DEVICE;
+    return type == MOE_T_BF16
+               ? backward<bf16_t>(maker(type), dy, x, w13, w2, const_cast<void*>(ac), kept,
+                                  ac_scales, T, d, inter, dac, h, dx, dw13, dw2, dev_status, st)
+               : backward<f16_t>(maker(type), dy, x, w13, w2, const_cast<void*>(ac), kept,
+                                 ac_scales, T, d, inter, dac, h, dx, dw13, dw2, dev_status, st);
+}

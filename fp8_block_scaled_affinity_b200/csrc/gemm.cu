@@ -2004,6 +2004,21 @@ bool make_out_map(CUtensorMap* m, void* base, uint64_t rows, uint64_t cols, bool
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2D map over [rows, cols] of any element type, rows pitch_bytes apart.
+bool make_map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t rows,
+                 uint64_t cols, uint64_t pitch_bytes, uint32_t box_rows,
+                 uint32_t box_cols, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promote) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {pitch_bytes};
+    cuuint32_t box[2] = {box_cols, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promote,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool device_is_sm100() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;

@@ -833,6 +833,38 @@ MOE_API int moe_gate_backward_ckpt(const MoeShape* shape, const uint16_t* dy, co
                                    const float* topk_score, float* dgate, float* du,
                                    int* dev_status, void* stream);
 
+/* ---------------------------------------------- dense gated block
+ * The block of the layers that have no experts, in bf16 or fp16: a = x W1^T,
+ * c = x W3^T, h = silu(a) c, y = h W2^T, and its backward pass.  fp32
+ * accumulation; h, and in the backward pass h and [da | dc], are rounded to
+ * `type` between two products.
+ *   type     MOE_T_BF16 or MOE_T_F16, of every matrix except 8-bit ac
+ *   T        tokens (0 .. 2^24); d, inter: multiples of 8 (8 .. 2^20)
+ *   x, y     [T, d];  w13 [2 inter, d], W1 (gate) above W3 (up);
+ *            w2 [d, inter];  all pointers 16-byte aligned
+ *   h        [T, inter] out: the hidden values (scratch for the caller who
+ *            needs no more than y)
+ *   ac       a and c kept for moe_ffn_backward, or NULL:
+ *            ac_type MOE_T_CKPT: uint8 [T, 2 W], W = inter rounded up to 128,
+ *            the codes of a, then from column W those of c, and ac_scales
+ *            fp32 [2 W / 128, T], by moe_ckpt_pack's rule (from the fp32
+ *            accumulator);  ac_type == type: [T, 2 inter], ac_scales unused.
+ * moe_ffn_backward: dh = dy W2, [da | dc] from dh and the kept a and c, then
+ *   dx = da W1 + dc W3 [T, d], dw13 = [da | dc]^T x [2 inter, d],
+ *   dw2 = dy^T h [d, inter], each in `type` and each NULL where not wanted
+ *   (w13 is read for dx only, x for dw13 only).  dac [T, 2 inter] and h
+ *   [T, inter] are written on the way: da and dc, and h of the kept values.
+ * T == 0: forward does nothing, backward writes zero weight gradients.
+ * Errors: MOE_ERR_ARG (types), MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_ALIGN,
+ * MOE_ERR_DEVICE, MOE_ERR_CUDA; MOE_DEV_TIMEOUT on dev_status. */
+MOE_API int moe_ffn_forward(const void* x, const void* w13, const void* w2, int type, int64_t T,
+                            int d, int inter, void* h, void* y, void* ac, int ac_type,
+                            float* ac_scales, int* dev_status, void* stream);
+MOE_API int moe_ffn_backward(const void* dy, const void* x, const void* w13, const void* w2,
+                             const void* ac, int ac_type, const float* ac_scales, int type,
+                             int64_t T, int d, int inter, void* dac, void* h, void* dx, void* dw13,
+                             void* dw2, int* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
