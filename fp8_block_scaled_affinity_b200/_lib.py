@@ -164,7 +164,7 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -571,14 +571,18 @@ _TYPES = {}
 
 def _type(t, name, kept=False) -> int:
     """Type code of a tensor; uint8 is a checkpoint's codes where `kept`."""
+    code = _types().get(t.dtype)
+    if code is None or (code == MOE_T_CKPT and not kept):
+        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+    return code
+
+
+def _types():
     if not _TYPES:
         import torch
         _TYPES.update({torch.float32: MOE_T_F32, torch.bfloat16: MOE_T_BF16,
                        torch.float16: MOE_T_F16, torch.uint8: MOE_T_CKPT})
-    code = _TYPES.get(t.dtype)
-    if code is None or (code == MOE_T_CKPT and not kept):
-        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
-    return code
+    return _TYPES
 
 
 def _mat(name, t, shape, dtype=None):
@@ -597,6 +601,37 @@ def _mat(name, t, shape, dtype=None):
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
 
 
+def _mats(first, *specs) -> int:
+    """_mat for (name, tensor, shape, dtype) of a whole call, in the few
+    attribute reads that a call of some microseconds can afford: the first
+    tensor's device is compared with the current one, the others' with its.
+    Returns the device index."""
+    name, t, shape, dtype = first
+    dev = t.get_device()
+    if dev < 0 or dev != _current_device() or t.shape != shape or not t.is_contiguous():
+        _mat(name, t, shape, dtype)
+    for name, t, shape, dtype in specs:
+        if t is not None and (t.get_device() != dev or t.dtype is not dtype or t.shape != shape
+                              or not t.is_contiguous()):
+            _mat(name, t, shape, dtype)
+    return dev
+
+
+def _current_device() -> int:
+    import torch
+    return torch._C._cuda_getDevice()
+
+
+def _f32():
+    import torch
+    return torch.float32
+
+
+def _u8():
+    import torch
+    return torch.uint8
+
+
 def _tiles(n) -> int:
     return (n + 127) // 128
 
@@ -609,19 +644,14 @@ def moe_layernorm_forward(x, weight, bias, eps, y, mean=None, rstd=None, dev_sta
                           stream=None):
     """y = layer norm of x [rows, cols]; weight, bias fp32 [cols] or None;
     mean, rstd fp32 [rows] out or None."""
-    import torch
-    f32 = torch.float32
-    ty = _type(x, "x")
+    ty, f32 = _type(x, "x"), _f32()
     rows, cols = x.shape
-    _mat("x", x, (rows, cols))
-    _mat("y", y, (rows, cols), x.dtype)
-    _mat("weight", weight, (cols,), f32)
-    _mat("bias", bias, (cols,), f32)
-    _mat("mean", mean, (rows,), f32)
-    _mat("rstd", rstd, (rows,), f32)
+    _mats(("x", x, (rows, cols), x.dtype), ("y", y, (rows, cols), x.dtype),
+          ("weight", weight, (cols,), f32), ("bias", bias, (cols,), f32),
+          ("mean", mean, (rows,), f32), ("rstd", rstd, (rows,), f32))
     _check("moe_layernorm_forward", lib().moe_layernorm_forward(
-        _ptr(x), ty, rows, cols, _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(mean),
-        _ptr(rstd), _ptr(dev_status), _stream(stream)))
+        _ptr(x), ty, rows, cols, _ptr(weight), _ptr(bias), eps, _ptr(y), _ptr(mean), _ptr(rstd),
+        _ptr(dev_status), _stream(stream)))
 
 
 def moe_layernorm_backward_workspace_size(rows, cols) -> int:
@@ -632,22 +662,17 @@ def moe_layernorm_backward(dy, x, x_scales, weight, mean, rstd, dx, dweight, dbi
                            dev_status=None, stream=None):
     """Gradients of moe_layernorm_forward.  x as the forward pass had it
     (x_scales None), or kept in 8 bits (uint8 codes and their x_scales)."""
-    import torch
-    f32 = torch.float32
-    ty, xt = _type(dy, "dy"), _type(x, "x", kept=True)
+    ty, xt, f32 = _type(dy, "dy"), _type(x, "x", kept=True), _f32()
     rows, cols = dy.shape
     kept = xt == MOE_T_CKPT
-    _mat("dy", dy, (rows, cols))
-    _mat("x", x, (rows, _wide(cols) if kept else cols))
     if kept == (x_scales is None):
         raise ValueError("x_scales goes with x kept in 8 bits")
-    _mat("x_scales", x_scales, (_tiles(cols), rows), f32)
-    _mat("weight", weight, (cols,), f32)
-    _mat("mean", mean, (rows,), f32)
-    _mat("rstd", rstd, (rows,), f32)
-    _mat("dx", dx, (rows, cols), dy.dtype)
-    _mat("dweight", dweight, (cols,), f32)
-    _mat("dbias", dbias, (cols,), f32)
+    _mats(("dy", dy, (rows, cols), dy.dtype),
+          ("x", x, (rows, _wide(cols) if kept else cols), x.dtype),
+          ("x_scales", x_scales, (_tiles(cols), rows), f32), ("weight", weight, (cols,), f32),
+          ("mean", mean, (rows,), f32), ("rstd", rstd, (rows,), f32),
+          ("dx", dx, (rows, cols), dy.dtype), ("dweight", dweight, (cols,), f32),
+          ("dbias", dbias, (cols,), f32))
     nbytes = ws.numel() * ws.element_size() if ws is not None else 0
     _check("moe_layernorm_backward", lib().moe_layernorm_backward(
         _ptr(dy), ty, _ptr(x), xt, _ptr(x_scales), rows, cols, _ptr(weight), _ptr(mean),
@@ -662,31 +687,34 @@ def moe_ckpt_row_bytes(cols) -> int:
 def moe_ckpt_pack(x, q, scales, dev_status=None, stream=None):
     """x [rows, cols] -> q uint8 [rows, moe_ckpt_row_bytes(cols)], scales fp32
     [ceil(cols / 128), rows]."""
-    import torch
     ty = _type(x, "x")
     rows, cols = x.shape
-    _mat("x", x, (rows, cols))
-    _mat("q", q, (rows, _wide(cols)), torch.uint8)
-    _mat("scales", scales, (_tiles(cols), rows), torch.float32)
+    _mats(("x", x, (rows, cols), x.dtype), ("q", q, (rows, _wide(cols)), _u8()),
+          ("scales", scales, (_tiles(cols), rows), _f32()))
     _check("moe_ckpt_pack", lib().moe_ckpt_pack(_ptr(x), ty, rows, cols, _ptr(q), _ptr(scales),
                                                 _ptr(dev_status), _stream(stream)))
 
 
 def moe_ckpt_unpack(q, scales, y, dev_status=None, stream=None):
     """The kept values as y [rows, cols] (its dtype)."""
-    import torch
     ty = _type(y, "y")
     rows, cols = y.shape
-    _mat("y", y, (rows, cols))
-    _mat("q", q, (rows, _wide(cols)), torch.uint8)
-    _mat("scales", scales, (_tiles(cols), rows), torch.float32)
+    _mats(("y", y, (rows, cols), y.dtype), ("q", q, (rows, _wide(cols)), _u8()),
+          ("scales", scales, (_tiles(cols), rows), _f32()))
     _check("moe_ckpt_unpack", lib().moe_ckpt_unpack(_ptr(q), _ptr(scales), rows, cols, _ptr(y), ty,
                                                     _ptr(dev_status), _stream(stream)))
 
 
 def moe_swiglu_backward_quant_ckpt(dh, ac_q, ac_scales, rows, inter, rows_total, q, q_scales,
                                    dev_status=None, stream=None):
-    """moe_swiglu_backward_quant from [a | c] kept in 8 bits."""
+    """moe_swiglu_backward_quant from [a | c] kept in 8 bits; dh [>= rows,
+    inter], the others rows_total rows."""
+    f32, u8, n = _f32(), _u8(), 2 * inter
+    _mats(("ac_q", ac_q, (rows_total, n), u8), ("ac_scales", ac_scales, (n // 128, rows_total), f32),
+          ("dh", dh, (dh.shape[0], inter), f32), ("q", q, (rows_total, n), u8),
+          ("q_scales", q_scales, (n // 128, rows_total), f32))
+    if dh.shape[0] < rows:
+        raise ValueError("dh: fewer rows than the call's")
     _check("moe_swiglu_backward_quant_ckpt", lib().moe_swiglu_backward_quant_ckpt(
         _ptr(dh), _ptr(ac_q), _ptr(ac_scales), int(rows), int(inter), int(rows_total), _ptr(q),
         _ptr(q_scales), _ptr(dev_status), _stream(stream)))
@@ -716,20 +744,19 @@ def moe_gate_backward_ckpt(shape, dy, o_q, o_scales, row_of_pair, topk_score, dg
         _ptr(topk_score), _ptr(dgate), _ptr(du), _ptr(dev_status), _stream(stream)))
 
 
-def _kept_ac(ac, ac_scales, dtype, T, inter) -> int:
-    """Checks a and c kept by moe_ffn_forward; their type code."""
-    import torch
+def _kept_ac(ac, ac_scales, dtype, T, inter):
+    """Type code of a and c kept by moe_ffn_forward, and what to check of them."""
     if ac is None:
         if ac_scales is not None:
             raise ValueError("ac_scales goes with ac in 8 bits")
-        return MOE_T_CKPT
-    kept = ac.dtype == torch.uint8
+        return MOE_T_CKPT, ()
+    kept = ac.dtype is _u8()
     if kept == (ac_scales is None):
         raise ValueError("ac_scales goes with ac in 8 bits")
-    w = _wide(inter) if kept else inter
-    _mat("ac", ac, (T, 2 * w), torch.uint8 if kept else dtype)
-    _mat("ac_scales", ac_scales, (2 * _tiles(inter), T), torch.float32)
-    return _type(ac, "ac", kept=True)
+    if not kept:
+        return _type(ac, "ac"), (("ac", ac, (T, 2 * inter), dtype),)
+    return MOE_T_CKPT, (("ac", ac, (T, 2 * _wide(inter)), ac.dtype),
+                        ("ac_scales", ac_scales, (2 * _tiles(inter), T), _f32()))
 
 
 def moe_ffn_forward(x, w13, w2, h, y, ac=None, ac_scales=None, dev_status=None, stream=None):
@@ -738,13 +765,10 @@ def moe_ffn_forward(x, w13, w2, h, y, ac=None, ac_scales=None, dev_status=None, 
     moe_ffn_backward, in 8 bits (uint8 and scales) or in x's type."""
     T, d = x.shape
     inter = w2.shape[1]
-    ty = _type(x, "x")
-    _mat("x", x, (T, d))
-    _mat("w13", w13, (2 * inter, d), x.dtype)
-    _mat("w2", w2, (d, inter), x.dtype)
-    _mat("h", h, (T, inter), x.dtype)
-    _mat("y", y, (T, d), x.dtype)
-    at = _kept_ac(ac, ac_scales, x.dtype, T, inter)
+    ty, t = _type(x, "x"), x.dtype
+    at, kept = _kept_ac(ac, ac_scales, t, T, inter)
+    _mats(("x", x, (T, d), t), ("w13", w13, (2 * inter, d), t), ("w2", w2, (d, inter), t),
+          ("h", h, (T, inter), t), ("y", y, (T, d), t), *kept)
     _check("moe_ffn_forward", lib().moe_ffn_forward(
         _ptr(x), _ptr(w13), _ptr(w2), ty, T, d, inter, _ptr(h), _ptr(y), _ptr(ac), at,
         _ptr(ac_scales), _ptr(dev_status), _stream(stream)))
@@ -756,19 +780,14 @@ def moe_ffn_backward(dy, x, w13, w2, ac, ac_scales, dac, h, dx=None, dw13=None, 
     and h [T, inter] are written on the way; dx, dw13, dw2 may be None."""
     T, d = dy.shape
     inter = w2.shape[1]
-    ty = _type(dy, "dy")
-    _mat("dy", dy, (T, d))
-    _mat("x", x, (T, d), dy.dtype)
-    _mat("w13", w13, (2 * inter, d), dy.dtype)
-    _mat("w2", w2, (d, inter), dy.dtype)
+    ty, t = _type(dy, "dy"), dy.dtype
     if ac is None:
         raise ValueError("moe_ffn_backward needs the kept ac")
-    at = _kept_ac(ac, ac_scales, dy.dtype, T, inter)
-    _mat("dac", dac, (T, 2 * inter), dy.dtype)
-    _mat("h", h, (T, inter), dy.dtype)
-    _mat("dx", dx, (T, d), dy.dtype)
-    _mat("dw13", dw13, (2 * inter, d), dy.dtype)
-    _mat("dw2", dw2, (d, inter), dy.dtype)
+    at, kept = _kept_ac(ac, ac_scales, t, T, inter)
+    _mats(("dy", dy, (T, d), t), ("x", x, (T, d), t), ("w13", w13, (2 * inter, d), t),
+          ("w2", w2, (d, inter), t), ("dac", dac, (T, 2 * inter), t), ("h", h, (T, inter), t),
+          ("dx", dx, (T, d), t), ("dw13", dw13, (2 * inter, d), t), ("dw2", dw2, (d, inter), t),
+          *kept)
     _check("moe_ffn_backward", lib().moe_ffn_backward(
         _ptr(dy), _ptr(x), _ptr(w13), _ptr(w2), _ptr(ac), at, _ptr(ac_scales), ty, T, d, inter,
         _ptr(dac), _ptr(h), _ptr(dx), _ptr(dw13), _ptr(dw2), _ptr(dev_status), _stream(stream)))

@@ -91,7 +91,9 @@ __global__ void __launch_bounds__(kThreads) ckpt_pack_kernel(const T* __restrict
 }
 
 // --------------------------------------------------------------- unpack
-// A thread takes 8 columns of UR rows: 8 codes in, 8 values out.
+// A thread takes 4 columns of UR rows: 4 codes in, 4 values out, so that a
+// warp's stores are whole lines in every type (with 8 columns its fp32 stores
+// are halves of twice as many: 261 us for 36864 rows of 7168).
 constexpr int UR = 4;
 
 template <class T, bool VEC>
@@ -99,38 +101,36 @@ __global__ void __launch_bounds__(kThreads) ckpt_unpack_kernel(const uint8_t* __
                                                                const float* __restrict__ scales,
                                                                int64_t rows, int64_t cols,
                                                                int64_t pitch, T* __restrict__ y) {
-    const int64_t chunks = (cols + 7) / 8;
-    const int64_t strips = (rows + UR - 1) / UR;
-    const int64_t u = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-    if (u >= strips * chunks) return;
-    const int64_t strip = u / chunks;
-    const int64_t c = (u - strip * chunks) * 8;
-    Raw<e4m3_t, 8> v[UR];
+    const int64_t c = (int64_t(blockIdx.y) * kThreads + threadIdx.x) * 4;
+    if (c >= cols) return;
+    const int64_t row0 = int64_t(blockIdx.x) * UR;
+    const int n = int(min(int64_t(UR), rows - row0));
+    uint32_t v[UR];
     float s[UR];
 #pragma unroll
     for (int r = 0; r < UR; ++r) {
-        const int64_t row = strip * UR + r;
-        v[r] = raw_zero<e4m3_t, 8>();
+        v[r] = 0u;
         s[r] = 0.0f;
-        if (row < rows) {
-            v[r] = raw_load<e4m3_t, 8>(reinterpret_cast<const e4m3_t*>(q) + row * pitch + c);
-            s[r] = __ldg(scales + c / kTile * rows + row);
+        if (r < n) {
+            v[r] = __ldcs(reinterpret_cast<const uint32_t*>(q + (row0 + r) * pitch + c));
+            s[r] = __ldg(scales + c / kTile * rows + row0 + r);
         }
     }
 #pragma unroll
     for (int r = 0; r < UR; ++r) {
-        const int64_t row = strip * UR + r;
-        if (row >= rows) break;
-        float f[8];
-        raw_floats(v[r], f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= s[r];
+        if (r >= n) break;
+        float2 f[2] = {e4m3x2_to_float2(uint16_t(v[r] & 0xFFFFu)),
+                       e4m3x2_to_float2(uint16_t(v[r] >> 16))};
+        f[0] = mul2(f[0], both(s[r]));
+        f[1] = mul2(f[1], both(s[r]));
+        T* o = y + (row0 + r) * cols + c;
         if (VEC) {
-            store_floats(y + row * cols + c, f);
+            store_pairs(o, f);
         } else {
+            const float g[4] = {f[0].x, f[0].y, f[1].x, f[1].y};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (c + i < cols) elem_store(y + row * cols + c + i, f[i]);
+            for (int i = 0; i < 4; ++i)
+                if (c + i < cols) elem_store(o + i, g[i]);
         }
     }
 }
@@ -138,94 +138,95 @@ __global__ void __launch_bounds__(kThreads) ckpt_unpack_kernel(const uint8_t* __
 // ------------------------------------- SwiGLU backward from a checkpoint
 // da = dh c s (1 + a (1 - s)), dc = dh a s with s = sigmoid(a), from dh
 // (fp32) and the kept [a | c]; the row [da | dc] quantised in 1x128 tiles.
-// A CTA takes 32 rows of one 128-feature tile of a and of c: 16 lanes hold a
-// row's tile, 8 features each, so da's and dc's amax are four shuffles.
+// A CTA takes 32 rows of one 128-feature tile of a and of c, a warp a row at
+// a time, 4 features a lane (whole lines of dh), four rows' loads in flight.
 // Scales of the strip, read and written, go through shared memory as lines.
+// Close to both limits: per 8 bytes a feature about 24 instructions.
 __global__ void __launch_bounds__(kThreads) swiglu_backward_ckpt_kernel(
     const float* __restrict__ dh, const uint8_t* __restrict__ ac,
     const float* __restrict__ ac_scales, int64_t rows, int I, int64_t rows_total,
     uint8_t* __restrict__ q, float* __restrict__ qs) {
     __shared__ float sin[2][kStripRows], sout[2][kStripRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane & 15, half = lane >> 4;
     const int nt = I / kTile;
     const int tile = blockIdx.x % nt;
     const int64_t row0 = int64_t(blockIdx.x / nt) * kStripRows;
-    if (warp < 2) {
-        const int64_t row = row0 + lane;
+    const int n = int(min(int64_t(kStripRows), rows - row0));
+    constexpr int RW = kStripRows / (kThreads / 32);  // rows of a warp
+    float4 hv[RW];
+    uint32_t av[RW], cv[RW];
+    const int f0 = tile * kTile + 4 * lane;
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+        const int lr = warp * RW + r;
+        hv[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        av[r] = cv[r] = 0u;
+        if (lr < n) {
+            const uint8_t* acr = ac + (row0 + lr) * 2 * I + f0;
+            hv[r] = __ldcs(reinterpret_cast<const float4*>(dh + (row0 + lr) * I + f0));
+            av[r] = __ldcs(reinterpret_cast<const uint32_t*>(acr));
+            cv[r] = __ldcs(reinterpret_cast<const uint32_t*>(acr + I));
+        }
+    }
+    if (warp < 2)
         sin[warp][lane] =
-            row < rows ? ac_scales[int64_t(warp * nt + tile) * rows_total + row] : 0.0f;
-    }
-    constexpr int RW = kStripRows / (kThreads / 32) / 2;  // row pairs of a warp
-    Raw<float, 8> hv[RW];
-    Raw<e4m3_t, 8> av[RW], cv[RW];
-    const int f0 = tile * kTile + 8 * sub;
-#pragma unroll
-    for (int r = 0; r < RW; ++r) {
-        const int64_t row = row0 + (warp * RW + r) * 2 + half;
-        hv[r] = raw_zero<float, 8>();
-        av[r] = cv[r] = raw_zero<e4m3_t, 8>();
-        if (row < rows) {
-            const e4m3_t* acr = reinterpret_cast<const e4m3_t*>(ac) + row * 2 * I + f0;
-            hv[r] = raw_load<float, 8>(dh + row * I + f0);
-            av[r] = raw_load<e4m3_t, 8>(acr);
-            cv[r] = raw_load<e4m3_t, 8>(acr + I);
-        }
-    }
+            lane < n ? ac_scales[int64_t(warp * nt + tile) * rows_total + row0 + lane] : 0.0f;
     __syncthreads();
+    float2 da[RW][2], dc[RW][2];
+    float amax = 0.0f;  // lane 2 r: da's of row r, lane 2 r + 1: dc's
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
-        const int lr = (warp * RW + r) * 2 + half;
-        const int64_t row = row0 + lr;
-        const float sa = sin[0][lr], sc = sin[1][lr];
-        float h[8], a[8], c[8];
-        raw_floats(hv[r], h);
-        raw_floats(av[r], a);
-        raw_floats(cv[r], c);
-        float ma = 0.0f, mc = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = a[i] * sa;
-            const float sg = __fdividef(1.0f, 1.0f + __expf(-x));
-            const float hs = h[i] * sg;
-            a[i] = hs * (c[i] * sc) * fmaf(x, 1.0f - sg, 1.0f);
-            c[i] = hs * x;
-            ma = fmaxf(ma, fabsf(a[i]));
-            mc = fmaxf(mc, fabsf(c[i]));
-        }
-#pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) {
-            ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
-            mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, o));
-        }
-        float s0, i0, s1, i1;
-        scale_from_amax(ma, s0, i0);
-        scale_from_amax(mc, s1, i1);
-        uint32_t wa[2], wc[2];
+        const int lr = warp * RW + r;
+        const float2 sa = both(sin[0][lr]), sc = both(sin[1][lr]);
+        const float2 h[2] = {make_float2(hv[r].x, hv[r].y), make_float2(hv[r].z, hv[r].w)};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            wa[i] = e4m3x2(__fmul_rn(a[4 * i], i0), __fmul_rn(a[4 * i + 1], i0)) |
-                    (uint32_t(e4m3x2(__fmul_rn(a[4 * i + 2], i0), __fmul_rn(a[4 * i + 3], i0)))
-                     << 16);
-            wc[i] = e4m3x2(__fmul_rn(c[4 * i], i1), __fmul_rn(c[4 * i + 1], i1)) |
-                    (uint32_t(e4m3x2(__fmul_rn(c[4 * i + 2], i1), __fmul_rn(c[4 * i + 3], i1)))
-                     << 16);
+            const float2 a = mul2(e4m3x2_to_float2(uint16_t(av[r] >> (16 * i))), sa);
+            const float2 c = mul2(e4m3x2_to_float2(uint16_t(cv[r] >> (16 * i))), sc);
+            const float2 e = add2(make_float2(__expf(-a.x), __expf(-a.y)), both(1.0f));
+            const float2 s = make_float2(__fdividef(1.0f, e.x), __fdividef(1.0f, e.y));
+            const float2 hs = mul2(h[i], s);
+            const float2 t = fma2(a, fma2(s, both(-1.0f), both(1.0f)), both(1.0f));
+            da[r][i] = mul2(mul2(hs, c), t);
+            dc[r][i] = mul2(hs, a);
         }
-        if (row < rows) {
-            uint8_t* o = q + row * 2 * I + f0;
-            *reinterpret_cast<uint2*>(o) = make_uint2(wa[0], wa[1]);
-            *reinterpret_cast<uint2*>(o + I) = make_uint2(wc[0], wc[1]);
+        const float ma = fmaxf(fmaxf(fabsf(da[r][0].x), fabsf(da[r][0].y)),
+                               fmaxf(fabsf(da[r][1].x), fabsf(da[r][1].y)));
+        const float mc = fmaxf(fmaxf(fabsf(dc[r][0].x), fabsf(dc[r][0].y)),
+                               fmaxf(fabsf(dc[r][1].x), fabsf(dc[r][1].y)));
+        // the warp's maxima: as integers, whose order is that of |v|
+        const uint32_t wa = __reduce_max_sync(0xffffffffu, __float_as_uint(ma));
+        const uint32_t wc = __reduce_max_sync(0xffffffffu, __float_as_uint(mc));
+        if (lane == 2 * r) amax = __uint_as_float(wa);
+        if (lane == 2 * r + 1) amax = __uint_as_float(wc);
+    }
+    // the divisions of all the warp's tiles at once, a tile a lane
+    float scale, inv;
+    scale_from_amax(amax, scale, inv);
+    if (lane < 2 * RW) sout[lane & 1][warp * RW + (lane >> 1)] = scale;
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+        const int lr = warp * RW + r;
+        const float2 i0 = both(__shfl_sync(0xffffffffu, inv, 2 * r));
+        const float2 i1 = both(__shfl_sync(0xffffffffu, inv, 2 * r + 1));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            da[r][i] = mul2(da[r][i], i0);
+            dc[r][i] = mul2(dc[r][i], i1);
         }
-        if (sub == 0) {
-            sout[0][lr] = s0;
-            sout[1][lr] = s1;
+        if (lr < n) {
+            uint8_t* o = q + (row0 + lr) * 2 * I + f0;
+            __stcs(reinterpret_cast<uint32_t*>(o),
+                   e4m3x2(da[r][0].x, da[r][0].y) |
+                       (uint32_t(e4m3x2(da[r][1].x, da[r][1].y)) << 16));
+            __stcs(reinterpret_cast<uint32_t*>(o + I),
+                   e4m3x2(dc[r][0].x, dc[r][0].y) |
+                       (uint32_t(e4m3x2(dc[r][1].x, dc[r][1].y)) << 16));
         }
     }
     __syncthreads();
-    if (warp < 2) {
-        const int64_t row = row0 + lane;
-        if (row < rows) qs[int64_t(warp * nt + tile) * rows_total + row] = sout[warp][lane];
-    }
+    if (warp < 2 && lane < n)
+        qs[int64_t(warp * nt + tile) * rows_total + row0 + lane] = sout[warp][lane];
 }
 
 template <class T>
@@ -247,16 +248,19 @@ int pack_any(const void* x, int64_t rows, int64_t cols, uint8_t* q, float* scale
 template <class T>
 int unpack_any(const uint8_t* q, const float* scales, int64_t rows, int64_t cols, void* y,
                cudaStream_t st) {
-    const int64_t units = (rows + UR - 1) / UR * ((cols + 7) / 8);
-    const int64_t grid = (units + kThreads - 1) / kThreads;
-    if (grid > INT32_MAX) return MOE_ERR_SHAPE;
+    const int64_t gx = (rows + UR - 1) / UR;
+    const int64_t gy = (cols + 4 * kThreads - 1) / (4 * kThreads);
+    if (gy > 65535) return MOE_ERR_SHAPE;
+    const dim3 grid{unsigned(gx), unsigned(gy)};
+    // a CTA no wider than the row
+    const int threads = int(std::min<int64_t>(kThreads, ((cols + 3) / 4 + 31) / 32 * 32));
     T* yp = static_cast<T*>(y);
-    if (cols % 8 == 0 && aligned16(y))
-        ckpt_unpack_kernel<T, true><<<unsigned(grid), kThreads, 0, st>>>(
-            q, scales, rows, cols, ckpt_row_bytes(cols), yp);
+    if (cols % 4 == 0 && aligned16(y))
+        ckpt_unpack_kernel<T, true><<<grid, threads, 0, st>>>(q, scales, rows, cols,
+                                                              ckpt_row_bytes(cols), yp);
     else
-        ckpt_unpack_kernel<T, false><<<unsigned(grid), kThreads, 0, st>>>(
-            q, scales, rows, cols, ckpt_row_bytes(cols), yp);
+        ckpt_unpack_kernel<T, false><<<grid, threads, 0, st>>>(q, scales, rows, cols,
+                                                               ckpt_row_bytes(cols), yp);
     return check_launch();
 }
 

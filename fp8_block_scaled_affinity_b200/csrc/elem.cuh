@@ -33,6 +33,31 @@ __device__ __forceinline__ float e4m3_to_float(uint8_t code) {
     return e4m3x2_to_float2(uint16_t(code)).x;
 }
 
+// Two fp32 values in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // Scale rule of the checkpoints: scale = fp32(amax / 448), inverse =
 // fp32(448 fp32(1 / amax)), both 1 for a tile of zeros.  (The online
 // quantisers round 448 / amax once; here one reciprocal and one product are
@@ -48,13 +73,16 @@ __device__ __forceinline__ void kept_scale(float amax, float& scale, float& inv)
     }
 }
 
-// Raw storage of 8 elements (or of one, for rows that are not 16-byte
-// aligned), kept packed until it is used.
+// Raw storage of 8 or 4 elements (or of one, for rows that are not aligned),
+// kept packed until it is used.
 template <class T, int E> struct Raw;
 template <> struct Raw<float, 8> { float4 a, b; };
 template <> struct Raw<bf16_t, 8> { uint4 a; };
 template <> struct Raw<f16_t, 8> { uint4 a; };
 template <> struct Raw<e4m3_t, 8> { uint2 a; };
+template <> struct Raw<float, 4> { float4 a; };
+template <> struct Raw<bf16_t, 4> { uint2 a; };
+template <> struct Raw<f16_t, 4> { uint2 a; };
 template <class T> struct Raw<T, 1> { T a; };
 
 template <class T, int E>
@@ -62,6 +90,9 @@ __device__ __forceinline__ Raw<T, E> raw_load(const T* p) {
     Raw<T, E> r;
     if constexpr (E == 1) {
         r.a = *p;
+    } else if constexpr (E == 4) {
+        if constexpr (sizeof(T) == 4) r.a = __ldg(reinterpret_cast<const float4*>(p));
+        else r.a = __ldg(reinterpret_cast<const uint2*>(p));
     } else if constexpr (sizeof(T) == 4) {
         r.a = __ldg(reinterpret_cast<const float4*>(p));
         r.b = __ldg(reinterpret_cast<const float4*>(p) + 1);
@@ -69,6 +100,20 @@ __device__ __forceinline__ Raw<T, E> raw_load(const T* p) {
         r.a = __ldg(reinterpret_cast<const uint4*>(p));
     } else {
         r.a = __ldg(reinterpret_cast<const uint2*>(p));
+    }
+    return r;
+}
+
+// The same of data read once, which is not kept in L1 before what is read
+// again; and stores of data that this kernel does not read.
+template <class T, int E>
+__device__ __forceinline__ Raw<T, E> raw_load_once(const T* p) {
+    Raw<T, E> r;
+    if constexpr (E == 4) {
+        if constexpr (sizeof(T) == 4) r.a = __ldcs(reinterpret_cast<const float4*>(p));
+        else r.a = __ldcs(reinterpret_cast<const uint2*>(p));
+    } else {
+        r = raw_load<T, E>(p);
     }
     return r;
 }
@@ -147,6 +192,33 @@ __device__ __forceinline__ void store_floats(T* p, const float (&f)[8]) {
             make_uint4(pack2t(T(), f[0], f[1]), pack2t(T(), f[2], f[3]), pack2t(T(), f[4], f[5]),
                        pack2t(T(), f[6], f[7]));
     }
+}
+
+// Pairs of 4 elements, or one element and a zero.
+__device__ __forceinline__ void raw_pairs(const Raw<float, 4>& r, float2 (&f)[2]) {
+    f[0] = make_float2(r.a.x, r.a.y);
+    f[1] = make_float2(r.a.z, r.a.w);
+}
+template <class T>
+__device__ __forceinline__ void raw_pairs(const Raw<T, 4>& r, float2 (&f)[2]) {
+    unpack2f(T(), r.a.x, f[0].x, f[0].y);
+    unpack2f(T(), r.a.y, f[1].x, f[1].y);
+}
+template <class T>
+__device__ __forceinline__ void raw_pairs(const Raw<T, 1>& r, float2 (&f)[1]) {
+    f[0] = make_float2(elem_float(r.a), 0.0f);
+}
+template <class T>
+__device__ __forceinline__ void store_pairs(T* p, const float2 (&f)[2]) {
+    if constexpr (sizeof(T) == 4)
+        __stcs(reinterpret_cast<float4*>(p), make_float4(f[0].x, f[0].y, f[1].x, f[1].y));
+    else
+        __stcs(reinterpret_cast<uint2*>(p),
+               make_uint2(pack2t(T(), f[0].x, f[0].y), pack2t(T(), f[1].x, f[1].y)));
+}
+template <class T>
+__device__ __forceinline__ void store_pairs(T* p, const float2 (&f)[1]) {
+    elem_store(p, f[0].x);
 }
 
 }  // namespace moe

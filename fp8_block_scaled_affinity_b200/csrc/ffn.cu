@@ -22,6 +22,15 @@
 // list of tiles, so that the last round of tiles is left part empty once and
 // not three times.
 //
+// Few tokens leave most pairs without a tile, and one token's work is reading
+// the weights once.  There the operands change places (few_kernel): 128 rows
+// of weights are the M side, up to 256 tokens the N side, and a cluster of up
+// to eight CTAs splits K, so that every SM streams weights; the partial sums
+// meet in shared memory across the cluster, in a fixed order.  One to four
+// tokens are matrix-vector products on the CUDA cores (vec_kernel).  In both
+// forms the second product's kernel starts under the first's end and fetches
+// weights before it waits for h.
+//
 // Accumulators are fp32.  h and [da | dc] are rounded to the operands' type
 // between two products (the tensor cores take 16-bit operands); everything
 // else is rounded once, on output.  Bound by the tensor cores for hundreds of
@@ -521,6 +530,332 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
     }
 }
 
+// ================================================== few tokens: split K
+// out[t, r] = sum_k W[r, k] x[t, k] for 128 rows r of W a CTA: W is the M side
+// of the MMA (a row per TMEM lane), nt tokens the N side.  GATED: 64 rows of
+// W1 in lanes 0-63 and the same 64 of W3 in lanes 64-127.
+//   warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 move the accumulator
+//   into shared memory (over the stages, all consumed by then); then every
+//   CTA of the cluster adds up its share of the tokens, ranks in order.
+constexpr int kFewThreads = 192;
+constexpr int kFewMaxStages = 12;
+constexpr int kFewRing1 = 200 * 1024;  // stages of a CTA alone on its SM,
+constexpr int kFewRing2 = 106 * 1024;  // and of two on one
+constexpr int kFewShared = 64;         // tokens up to which two share an SM
+constexpr int kFewMaxTokens = 256;  // N side of one tile
+constexpr int kFewMaxSplit = 8;     // portable cluster size
+
+struct FewArgs {
+    CUtensorMap w, x;
+    void* out;
+    int rows;       // output columns (W2's rows, or features)
+    int pitch;      // of out
+    int w3;         // GATED: first row of W3
+    int64_t tokens;
+    int nt;         // tokens of a tile, a multiple of 16
+    int tiles_w;
+    int nkb;
+    int ring;       // bytes of the stages
+    int stages;
+    int wait_first; // 1: x comes from the kernel before this one
+    int* dev_status;
+    uint64_t wait_limit_ns;
+};
+
+struct FewShared {
+    uint64_t full[kFewMaxStages];
+    uint64_t empty[kFewMaxStages];
+    uint64_t done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+constexpr size_t few_smem(int ring) { return size_t(ring) + sizeof(FewShared) + 1024; }
+static_assert(kFewMaxTokens * 128 * 4 <= kFewRing1 && kFewShared * 128 * 4 <= kFewRing2,
+              "the partial sums lie over the stages");
+static_assert(few_smem(kFewRing1) <= 232448 && 2 * (few_smem(kFewRing2) + 1024) <= 233472,
+              "shared memory of an SM");
+
+// The sums of this CTA's share of the tile over the cluster's partial sums,
+// ranks in order, and the output.  A warp takes 64 columns of a token at a
+// time, two a lane; eight ranks' loads, or several tokens' of fewer ranks, are
+// in flight together.
+template <bool GATED, class T, int SPLIT>
+__device__ __forceinline__ void few_sum(const FewArgs& a, uint32_t part, int rank, int wt,
+                                        int64_t t0) {
+    constexpr int kBatch = 8 / SPLIT;
+    constexpr int kSteps = GATED ? 1 : 2;  // pieces of 64 output columns
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int step = SPLIT * (kFewThreads / 32);
+    const int items = int(min(int64_t(a.nt), a.tokens - t0)) * kSteps;  // (token, piece)
+    T* const out = static_cast<T*>(a.out);
+    uint32_t at[SPLIT];
+#pragma unroll
+    for (int k = 0; k < SPLIT; ++k) at[k] = mapa(part, k) + uint32_t(lane) * 8u;
+    for (int i0 = rank + SPLIT * warp; i0 < items; i0 += kBatch * step) {
+        float2 v[kBatch][SPLIT], u[kBatch][SPLIT];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * step;
+            if (i < items) {
+                const uint32_t off = uint32_t((i / kSteps) * 128 + 64 * (i % kSteps)) * 4u;
+#pragma unroll
+                for (int k = 0; k < SPLIT; ++k) {
+                    v[j][k] = ld_cluster2(at[k] + off);
+                    if (GATED) u[j][k] = ld_cluster2(at[k] + off + 256u);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * step;
+            const int r = wt * (64 * kSteps) + 64 * (i % kSteps) + 2 * lane;
+            if (i < items && r < a.rows) {  // an even number: both columns exist
+                float2 s = v[j][0];
+#pragma unroll
+                for (int k = 1; k < SPLIT; ++k) {
+                    s.x += v[j][k].x;
+                    s.y += v[j][k].y;
+                }
+                if (GATED) {
+                    float2 c = u[j][0];
+#pragma unroll
+                    for (int k = 1; k < SPLIT; ++k) {
+                        c.x += u[j][k].x;
+                        c.y += u[j][k].y;
+                    }
+                    s.x = s.x * sigmoid_fast(s.x) * c.x;
+                    s.y = s.y * sigmoid_fast(s.y) * c.y;
+                }
+                *reinterpret_cast<uint32_t*>(out + (t0 + i / kSteps) * a.pitch + r) =
+                    pack2t(T(), s.x, s.y);
+            }
+        }
+    }
+}
+
+template <bool GATED, class T>
+__global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    FewShared* ss = reinterpret_cast<FewShared*>(smem + a.ring);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x, split = gridDim.x;  // the cluster is the x row of the grid
+    const int wt = blockIdx.y;
+    const int64_t t0 = int64_t(blockIdx.z) * a.nt;
+    // this CTA's part of K
+    const int kb0 = int(int64_t(a.nkb) * rank / split);
+    const int n = int(int64_t(a.nkb) * (rank + 1) / split) - kb0;
+    const uint32_t cols = a.nt <= 32 ? 32 : a.nt <= 64 ? 64 : a.nt <= 128 ? 128 : 256;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(smem_u32(&ss->full[s]), 1);
+            mbar_init(smem_u32(&ss->empty[s]), 1);
+        }
+        mbar_init(smem_u32(&ss->done), 1);
+        ss->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&ss->tmem_base), cols);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    launch_dependents();
+    const uint32_t tmem = ss->tmem_base;
+    const int stage_bytes = kOperandBytes + a.nt * 128;
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            const int w0 = wt * (GATED ? 64 : 128);
+            auto load_w = [&](int i) {
+                const int s = i % a.stages, k0 = (kb0 + i) * kTileK;
+                const uint32_t bar = smem_u32(&ss->full[s]);
+                const uint32_t dst = smem_u32(smem + size_t(s) * stage_bytes);
+                mbar_arrive_expect_tx(bar, uint32_t(stage_bytes));
+                tma_load_2d(dst, &a.w, bar, k0, w0);
+                if (GATED) tma_load_2d(dst + kOperandBytes / 2, &a.w, bar, k0, a.w3 + w0);
+            };
+            auto load_x = [&](int i) {
+                const int s = i % a.stages;
+                tma_load_2d(smem_u32(smem + size_t(s) * stage_bytes) + kOperandBytes, &a.x,
+                            smem_u32(&ss->full[s]), (kb0 + i) * kTileK, int(t0));
+            };
+            // the first stages: weights before the wait, tokens after it
+            const int first = min(n, a.stages);
+            for (int i = 0; i < first; ++i) load_w(i);
+            if (a.wait_first) wait_dependencies();
+            for (int i = 0; i < first; ++i) load_x(i);
+            int i = first;
+            for (; i < n; ++i) {
+                ok = mbar_wait(smem_u32(&ss->empty[i % a.stages]), ((i / a.stages) & 1u) ^ 1u,
+                               &ss->abort_flag, a.dev_status, a.wait_limit_ns);
+                if (!ok) break;
+                load_w(i);
+                load_x(i);
+            }
+            if (!ok)  // loads in flight land before the CTA leaves
+                for (int j = max(0, i - a.stages); j < i; ++j)
+                    mbar_quiesce(smem_u32(&ss->full[j % a.stages]), (j / a.stages) & 1u, nullptr,
+                                 a.wait_limit_ns);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc =
+                idesc_f16(std::is_same<T, bf16_t>::value, 0, 0, 128, a.nt);
+            for (int i = 0; i < n; ++i) {
+                const int s = i % a.stages;
+                ok = mbar_wait(smem_u32(&ss->full[s]), (i / a.stages) & 1u, &ss->abort_flag,
+                               a.dev_status, a.wait_limit_ns);
+                if (!ok) break;
+                fence_after();
+                const uint32_t sa = smem_u32(smem + size_t(s) * stage_bytes);
+                uint64_t ad = sw128_desc16(sa, 16), bd = sw128_desc16(sa + kOperandBytes, 16);
+#pragma unroll
+                for (int kk = 0; kk < kTileK / 16; ++kk, ad += 2, bd += 2)
+                    mma_f16(tmem, ad, bd, idesc, (i | kk) ? 1u : 0u);
+                commit(smem_u32(&ss->empty[s]));
+            }
+            commit(smem_u32(&ss->done));
+            mbar_quiesce(smem_u32(&ss->done), 0, nullptr, a.wait_limit_ns);
+        }
+    }
+    __syncwarp();
+    // the products are done (warp 1 has waited for them), or given up
+    const bool bad = __syncthreads_or(!ok || *reinterpret_cast<volatile int*>(&ss->abort_flag));
+    fence_after();
+    float* part = reinterpret_cast<float*>(smem);  // [nt][128]
+    if (warp >= 2) {
+        const int q = warp & 3;
+        for (int c = 0; c < a.nt; c += 16) {
+            uint32_t v[16];
+            if (n > 0) {
+                tmem_ld16(tmem + (uint32_t(q * 32) << 16) + c, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part[(c + i) * 128 + q * 32 + lane] = __uint_as_float(v[i]);
+        }
+        fence_before();
+    }
+    cluster_sync();  // every CTA's partial sums are in place
+    if (!bad) {
+        if (split == 1) few_sum<GATED, T, 1>(a, smem_u32(part), rank, wt, t0);
+        else if (split == 2) few_sum<GATED, T, 2>(a, smem_u32(part), rank, wt, t0);
+        else if (split == 4) few_sum<GATED, T, 4>(a, smem_u32(part), rank, wt, t0);
+        else few_sum<GATED, T, 8>(a, smem_u32(part), rank, wt, t0);
+    }
+    cluster_sync();  // nobody's partial sums are read any more
+    if (warp == 1) {
+        fence_after();
+        tmem_free(tmem, cols);
+    }
+}
+
+// ================================================== one to four tokens
+// Matrix-vector products on the CUDA cores: reading the weights once is all
+// the work there is, and plain 16-byte loads of whole rows, many in flight in
+// every warp, start and end sooner than a pipeline of tiles.  A warp takes a
+// part of one output's K (GATED: of the feature's rows of W1 and of W3): 256
+// elements a step, kVecSteps steps' weights in flight; tokens come through L1.
+// Four warps a CTA; `parts` warps share an output and meet in shared memory.
+constexpr int kVecWarps = 4;
+constexpr int kVecSteps = 4;
+constexpr int kVecTokens = 4;
+
+template <class T>
+__device__ __forceinline__ uint4 ld_plain(const T* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+template <bool GATED, int TOK, class T>
+__global__ void __launch_bounds__(kVecWarps * 32)
+    vec_kernel(const T* __restrict__ w, const T* x, T* __restrict__ out, int tokens, int rows,
+               int K, int parts, int wait_first) {
+    constexpr int R = GATED ? 2 : 1;
+    __shared__ float part[kVecWarps][R * TOK];
+    launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.x * (kVecWarps / parts) + warp / parts;
+    const bool have = row < rows;
+    const int steps = (K + 255) / 256;
+    const int s0 = steps * (warp % parts) / parts, s1 = steps * (warp % parts + 1) / parts;
+    const T* wr[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) wr[r] = w + (int64_t(have ? row : 0) + int64_t(r) * rows) * K;
+    float acc[R][TOK];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) acc[r][t] = 0.0f;
+    for (int b = s0; b < s1; b += kVecSteps) {
+        uint4 v[R][kVecSteps];
+#pragma unroll
+        for (int i = 0; i < kVecSteps; ++i) {
+            const int k = (b + i) * 256 + lane * 8;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                v[r][i] = b + i < s1 && k < K && have
+                              ? __ldcs(reinterpret_cast<const uint4*>(wr[r] + k))
+                              : make_uint4(0u, 0u, 0u, 0u);
+        }
+        // the first weights are on their way before the values they wait for
+        if (wait_first && b == s0) wait_dependencies();
+#pragma unroll
+        for (int i = 0; i < kVecSteps; ++i) {
+            const int k = (b + i) * 256 + lane * 8;
+            if (b + i < s1 && k < K) {
+                float wf[R][8];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    Raw<T, 8> raw;
+                    raw.a = v[r][i];
+                    raw_floats(raw, wf[r]);
+                }
+#pragma unroll
+                for (int t = 0; t < TOK; ++t) {
+                    if (TOK == 1 || t < tokens) {
+                        Raw<T, 8> raw;
+                        raw.a = ld_plain(x + int64_t(t) * K + k);
+                        float xf[8];
+                        raw_floats(raw, xf);
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                acc[r][t] = fmaf(wf[r][e], xf[e], acc[r][t]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) {
+            float a = acc[r][t];
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+            if (lane == 0) part[warp][r * TOK + t] = a;
+        }
+    __syncthreads();
+    if (have && warp % parts == 0 && lane < TOK && lane < tokens) {
+        float a = 0.0f, c = 0.0f;
+        for (int p = 0; p < parts; ++p) {
+            a += part[warp + p][lane];
+            if (GATED) c += part[warp + p][TOK * (R - 1) + lane];
+        }
+        if (GATED) a = a * sigmoid_fast(a) * c;
+        elem_store(out + int64_t(lane) * rows + row, a);
+    }
+}
+
 // -------------------------------------------------------------------- host
 // CTA pairs the device holds at once (cached per device).
 template <int EPI, int KEPT, class T>
@@ -614,33 +949,6 @@ Args make_args(int64_t T, int inter, int* dev_status) {
 }
 
 template <class T>
-int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t rows, int d, int I,
-            void* h, void* y, void* ac, int kept, float* ac_scales, int* dev_status,
-            cudaStream_t st) {
-    Args a = make_args(rows, I, dev_status);
-    product(a, mk, x, false, w13, false, h, rows, 2 * int64_t(I), d, 256);
-    // the gated tile: 128 features of W1 and of W3
-    Problem& p = a.p[0];
-    p.n = I;
-    p.tiles_n = (I + 127) / 128;
-    a.tiles = p.tiles_m * p.tiles_n;
-    mk.output(&p.out, h, rows, I, I);
-    a.ac = ac;
-    a.ac_scales = ac_scales;
-    if (kept == kKept16) {
-        mk.output(&a.o1, ac, rows, I, 2 * int64_t(I));
-        mk.output(&a.o2, static_cast<uint16_t*>(ac) + I, rows, I, 2 * int64_t(I));
-    }
-    Args b = make_args(rows, I, dev_status);
-    product(b, mk, h, false, w2, false, y, rows, d, I, 256);
-    if (!mk.ok) return MOE_ERR_CUDA;
-    const int rc = kept == kKept8    ? launch<kGated, kKept8, T>(a, st)
-                   : kept == kKept16 ? launch<kGated, kKept16, T>(a, st)
-                                     : launch<kGated, kKeptNone, T>(a, st);
-    return rc != MOE_OK ? rc : launch<kPlain, kKeptNone, T>(b, st);
-}
-
-template <class T>
 int backward(Maker mk, const void* dy, const void* x, const void* w13, const void* w2, void* ac,
              int kept, const float* ac_scales, int64_t rows, int d, int I, void* dac, void* h,
              void* dx, void* dw13, void* dw2, int* dev_status, cudaStream_t st) {
@@ -659,6 +967,167 @@ int backward(Maker mk, const void* dy, const void* x, const void* w13, const voi
     const int rc = kept == kKept8 ? launch<kBackward, kKept8, T>(a, st)
                                   : launch<kBackward, kKept16, T>(a, st);
     return rc != MOE_OK || b.n_problems == 0 ? rc : launch<kPlain, kKeptNone, T>(b, st);
+}
+
+// How a product with few tokens is laid out, and about how long it takes:
+// in SM clocks, a CTA's 16 x 16 x nt steps (2 nt clocks per 64 K elements; 128
+// is what the weights' bytes cost at least) and a fixed part for starting,
+// filling the pipeline and adding up.
+struct FewPlan {
+    int tiles_t, tiles_w, nt, split, ring;
+    int64_t clocks;
+};
+FewPlan few_plan(int64_t T, int rows, int rows_per_tile, int nkb) {
+    FewPlan p;
+    p.tiles_t = int((T + kFewMaxTokens - 1) / kFewMaxTokens);
+    p.nt = int(((T + p.tiles_t - 1) / p.tiles_t + 15) / 16 * 16);
+    p.tiles_w = (rows + rows_per_tile - 1) / rows_per_tile;
+    const int64_t tiles = int64_t(p.tiles_t) * p.tiles_w;
+    const int sms = sm_count();
+    // Up to 64 tokens two CTAs share an SM, so that one fetches while the
+    // other adds up, and the next product's start under this one: K is split
+    // until there are more CTAs than SMs (one token of d = 7168, inter = 2048:
+    // 22.9 us against 28.7 us with one CTA an SM).  Wider stages leave room
+    // for one: split until three quarters of the SMs have a CTA.
+    const bool two = p.nt <= kFewShared;
+    p.ring = two ? kFewRing2 : kFewRing1;
+    p.split = 1;
+    while (p.split < kFewMaxSplit && tiles * p.split * 4 < int64_t(sms) * (two ? 4 : 3) &&
+           nkb >= 8 * p.split)
+        p.split *= 2;
+    const int64_t waves = (tiles * p.split + sms - 1) / sms;
+    p.clocks = waves * (int64_t(nkb + p.split - 1) / p.split * std::max(2 * p.nt, 128) + 6000);
+    return p;
+}
+// Whether a plan beats pair tiles of 256 x 256: only where those leave pairs
+// idle, and then by the same estimate.
+bool few_better(const FewPlan& p, int64_t pair_tiles, int nkb) {
+    return pair_tiles < sm_count() / 2 && p.clocks < int64_t(nkb) * 512 + 5000;
+}
+
+template <bool GATED, int TOK, class T>
+int launch_vec_tok(const void* w, const void* x, void* out, int tokens, int rows, int K, bool after,
+                   cudaStream_t st) {
+    // Warps per output: as many as leave every warp one batch of steps, so
+    // that there are enough CTAs to even out over the SMs.
+    const int steps = (K + 255) / 256;
+    const int parts = steps > 2 * kVecSteps ? 4 : steps > kVecSteps ? 2 : 1;
+    const int per = kVecWarps / parts;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned((rows + per - 1) / per), 1, 1);
+    cfg.blockDim = dim3(kVecWarps * 32, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, vec_kernel<GATED, TOK, T>, static_cast<const T*>(w),
+                           static_cast<const T*>(x), static_cast<T*>(out), tokens, rows, K, parts,
+                           int(after)) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return check_launch();
+}
+template <bool GATED, class T>
+int launch_vec(const void* w, const void* x, void* out, int tokens, int rows, int K, bool after,
+               cudaStream_t st) {
+    return tokens == 1   ? launch_vec_tok<GATED, 1, T>(w, x, out, tokens, rows, K, after, st)
+           : tokens == 2 ? launch_vec_tok<GATED, 2, T>(w, x, out, tokens, rows, K, after, st)
+                         : launch_vec_tok<GATED, 4, T>(w, x, out, tokens, rows, K, after, st);
+}
+
+template <bool GATED, class T>
+int launch_few(Maker& mk, const FewPlan& p, const void* w, const void* x, void* out, int64_t tokens,
+               int rows, int K, int* dev_status, bool after, cudaStream_t st) {
+    FewArgs a = {};
+    mk.operand(&a.w, w, GATED ? 2 * int64_t(rows) : rows, K, GATED ? 64 : 128);
+    mk.operand(&a.x, x, tokens, K, p.nt);
+    if (!mk.ok) return MOE_ERR_CUDA;
+    a.out = out;
+    a.rows = rows;
+    a.pitch = rows;
+    a.w3 = rows;
+    a.tokens = tokens;
+    a.nt = p.nt;
+    a.tiles_w = p.tiles_w;
+    a.nkb = (K + kTileK - 1) / kTileK;
+    a.ring = p.ring;
+    a.stages = std::min(kFewMaxStages, p.ring / (kOperandBytes + p.nt * 128));
+    a.wait_first = after;
+    a.dev_status = dev_status;
+    a.wait_limit_ns = wait_limit_ns();
+    if (cudaFuncSetAttribute(few_kernel<GATED, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(few_smem(p.ring))) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(p.split), unsigned(p.tiles_w), unsigned(p.tiles_t));
+    cfg.blockDim = dim3(kFewThreads, 1, 1);
+    cfg.dynamicSmemBytes = few_smem(p.ring);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(p.split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, few_kernel<GATED, T>, a) != cudaSuccess) return MOE_ERR_CUDA;
+    return check_launch();
+}
+
+template <class T>
+int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t rows, int d, int I,
+            void* h, void* y, void* ac, int kept, float* ac_scales, int* dev_status,
+            cudaStream_t st) {
+    const int kd = (d + kTileK - 1) / kTileK, ki = (I + kTileK - 1) / kTileK;
+    const int64_t tiles_m = (rows + kTileM - 1) / kTileM;
+    const FewPlan fa = few_plan(rows, I, 64, kd), fb = few_plan(rows, d, 128, ki);
+    // few tokens: whichever way takes fewer clocks.  (One token, d = 7168,
+    // inter = 2048: 70 us in pairs of CTAs.)  What is kept comes from the pairs'
+    // epilogue, which sees 128 features of a and c together.
+    const bool few_a = kept == kKeptNone && few_better(fa, tiles_m * ((I + 127) / 128), kd);
+    const bool few_b = few_better(fb, tiles_m * ((d + 255) / 256), ki);
+    int rc;
+    // One token, or a few with few weights (a token's multiplications cost as
+    // much time as its weights' bytes: 2 and 4 tokens of 88 MB of weights take
+    // 25 and 36 us as vectors and 23 us as tiles, of 0.8 MB 3.4 and 9.3 us).
+    if (kept == kKeptNone && (rows == 1 || (rows <= kVecTokens &&
+                                            rows * 6 * int64_t(d) * I <= 100000000))) {
+        rc = launch_vec<true, T>(w13, x, h, int(rows), I, d, false, st);
+        return rc != MOE_OK ? rc : launch_vec<false, T>(w2, h, y, int(rows), d, I, true, st);
+    }
+    if (few_a) {
+        rc = launch_few<true, T>(mk, fa, w13, x, h, rows, I, d, dev_status, false, st);
+        if (rc != MOE_OK) return rc;
+        if (few_b) return launch_few<false, T>(mk, fb, w2, h, y, rows, d, I, dev_status, true, st);
+    }
+    Args a = make_args(rows, I, dev_status);
+    product(a, mk, x, false, w13, false, h, rows, 2 * int64_t(I), d, 256);
+    // the gated tile: 128 features of W1 and of W3
+    Problem& p = a.p[0];
+    p.n = I;
+    p.tiles_n = (I + 127) / 128;
+    a.tiles = p.tiles_m * p.tiles_n;
+    mk.output(&p.out, h, rows, I, I);
+    a.ac = ac;
+    a.ac_scales = ac_scales;
+    if (kept == kKept16) {
+        mk.output(&a.o1, ac, rows, I, 2 * int64_t(I));
+        mk.output(&a.o2, static_cast<uint16_t*>(ac) + I, rows, I, 2 * int64_t(I));
+    }
+    Args b = make_args(rows, I, dev_status);
+    product(b, mk, h, false, w2, false, y, rows, d, I, 256);
+    if (!mk.ok) return MOE_ERR_CUDA;
+    if (!few_a) {
+        rc = kept == kKept8    ? launch<kGated, kKept8, T>(a, st)
+             : kept == kKept16 ? launch<kGated, kKept16, T>(a, st)
+                               : launch<kGated, kKeptNone, T>(a, st);
+        if (rc != MOE_OK) return rc;
+    }
+    return few_b ? launch_few<false, T>(mk, fb, w2, h, y, rows, d, I, dev_status, false, st)
+                 : launch<kPlain, kKeptNone, T>(b, st);
 }
 
 int check_sizes(int type, int64_t T, int d, int inter) {

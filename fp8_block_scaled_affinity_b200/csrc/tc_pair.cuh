@@ -1,5 +1,5 @@
-// tcgen05 / TMA / cluster glue of kernels that run one MMA over a pair of
-// CTAs (cta_group::2) on 16-bit operands.  Operand tiles lie in shared memory
+// tcgen05 / TMA / cluster glue of the kernels on 16-bit operands: one MMA over
+// a pair of CTAs (cta_group::2), or over one CTA of a cluster.  Operand tiles lie in shared memory
 // with the 128-byte swizzle; every wait is bounded.
 #pragma once
 
@@ -142,6 +142,44 @@ __device__ __forceinline__ void pair_mma_f16(uint32_t d_tmem, uint64_t adesc, ui
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
 }
+// The same of one CTA (M = 128).
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     dst_smem),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
+                 : "memory");
+}
+
+// Programmatic dependent launch: the next kernel of the stream may be
+// scheduled from here on; and the wait for everything the kernels before
+// this one have written.
+__device__ __forceinline__ void launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_dependencies() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Floats of shared memory of a CTA of the cluster (mapa address).
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+    return v;
+}
+
 __device__ __forceinline__ void pair_commit(uint32_t bar) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
