@@ -37,9 +37,147 @@ from ._lib import (MOE_DEV_TIMEOUT, MOE_EPI_BF16, MOE_EPI_F32, MOE_EPI_SWIGLU_QU
                    moe_layernorm_backward_workspace_size, moe_ckpt_row_bytes, moe_ckpt_pack,
                    moe_ckpt_unpack, moe_swiglu_backward_quant_ckpt, moe_wgrad_quant_h_ckpt,
                    moe_wgrad_quant_dac_ckpt, moe_gate_backward_ckpt, moe_ffn_forward,
-                   moe_ffn_backward)
+                   moe_ffn_backward, moe_grouped_gemm_fp8_ckpt)
 
-__all__ = ["MoeLayer", "MoeShape", "MoeError", "lib", "make_shape", "moe_version"]
+__all__ = ["MoeLayer", "GatedFfn", "LayerNorm", "MoeShape", "MoeError", "lib", "make_shape", "moe_version"]
+
+
+def _check_keep(keep):
+    if keep not in ("full", "fp8"):
+        raise ValueError("keep must be 'full' or 'fp8'")
+
+
+def _pack(x, stream):
+    """x kept in 8 bits: (codes, scales)."""
+    import torch
+    rows, cols = x.shape
+    q = torch.empty((rows, moe_ckpt_row_bytes(cols)), dtype=torch.uint8, device=x.device)
+    s = torch.empty(((cols + 127) // 128, rows), dtype=torch.float32, device=x.device)
+    moe_ckpt_pack(x, q, s, stream=stream)
+    return q, s
+
+
+class LayerNorm:
+    """The normalisation in front of a layer: weight, bias (fp32 [cols] on the
+    GPU, or None) and what its backward pass needs of the last forward_train.
+
+    forward_train(x, keep): keep="full" keeps x itself (it must stay unchanged
+    until backward() has run), "fp8" an 8-bit copy of it.  backward(dy) leaves
+    the parameters' gradients in dweight and dbias (fp32)."""
+
+    def __init__(self, weight=None, bias=None, eps: float = 1e-5):
+        self.weight, self.bias, self.eps = weight, bias, float(eps)
+        self.dweight = self.dbias = None
+        self._kept = None
+
+    def forward(self, x, y=None, stream=None):
+        import torch
+        if y is None:
+            y = torch.empty_like(x)
+        moe_layernorm_forward(x, self.weight, self.bias, self.eps, y, stream=stream)
+        return y
+
+    def forward_train(self, x, y=None, keep: str = "full", stream=None):
+        """forward(), the same bits, keeping what backward() needs."""
+        import torch
+        _check_keep(keep)
+        if y is None:
+            y = torch.empty_like(x)
+        stats = [torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
+                 for _ in range(2)]
+        moe_layernorm_forward(x, self.weight, self.bias, self.eps, y, *stats, stream=stream)
+        self._kept = (_pack(x, stream) if keep == "fp8" else (x, None)) + tuple(stats)
+        return y
+
+    def backward(self, dy, stream=None):
+        """dx (dy's type) of the last forward_train(); dy of x's type or fp32."""
+        import torch
+        if self._kept is None:
+            raise RuntimeError("backward() needs a forward_train() first")
+        x, scales, mean, rstd = self._kept
+        rows, cols = dy.shape
+        dx = torch.empty_like(dy)
+        self.dweight = torch.empty((cols,), dtype=torch.float32, device=dy.device)
+        self.dbias = torch.empty_like(self.dweight)
+        ws = torch.empty((max(16, moe_layernorm_backward_workspace_size(rows, cols)),),
+                         dtype=torch.uint8, device=dy.device)
+        moe_layernorm_backward(dy, x, scales, self.weight, mean, rstd, dx, self.dweight,
+                               self.dbias, ws, stream=stream)
+        return dx
+
+
+class GatedFfn:
+    """The dense gated block of a layer without experts, in bf16 or fp16:
+    y = (silu(n W1^T) (n W3^T)) W2^T, n = norm(x) where a norm is given.
+
+    w13: [2I, d] (W1 above W3), w2: [d, I], on the GPU; T may differ from call
+    to call."""
+
+    def __init__(self, w13, w2, norm: Optional[LayerNorm] = None):
+        import torch
+        if tuple(w13.shape) != (2 * w2.shape[1], w2.shape[0]) or w13.dtype != w2.dtype:
+            raise ValueError("w13 must be [2I, d] and w2 [d, I] of one dtype")
+        self.w13, self.w2, self.norm = w13, w2, norm
+        self.dev_status = torch.zeros((1,), dtype=torch.int32, device=w2.device)
+        self._kept = None
+
+    def _hidden(self, x, cols):
+        import torch
+        return torch.empty((x.shape[0], cols), dtype=x.dtype, device=x.device)
+
+    def forward(self, x, y=None, stream=None):
+        """y for x [T, d] on the GPU."""
+        import torch
+        n = x if self.norm is None else self.norm.forward(x, stream=stream)
+        if y is None:
+            y = torch.empty_like(x)
+        moe_ffn_forward(n, self.w13, self.w2, self._hidden(x, self.w2.shape[1]), y,
+                        dev_status=self.dev_status, stream=stream)
+        return y
+
+    def forward_train(self, x, y=None, keep: str = "fp8", stream=None):
+        """forward(), keeping what backward() needs: the block's input (x, or
+        the norm's output) as it is, and gate and up, and the norm's input, in
+        8 bits ("fp8") or as they are ("full").  x must stay unchanged until
+        backward() has run, unless it goes through a norm and keep is "fp8"."""
+        import torch
+        _check_keep(keep)
+        T, inter = x.shape[0], self.w2.shape[1]
+        n = x if self.norm is None else self.norm.forward_train(x, keep=keep, stream=stream)
+        if y is None:
+            y = torch.empty_like(x)
+        if keep == "fp8":
+            wide = 2 * moe_ckpt_row_bytes(inter)
+            ac = torch.empty((T, wide), dtype=torch.uint8, device=x.device)
+            scales = torch.empty((wide // 128, T), dtype=torch.float32, device=x.device)
+        else:
+            ac, scales = self._hidden(x, 2 * inter), None
+        moe_ffn_forward(n, self.w13, self.w2, self._hidden(x, inter), y, ac, scales,
+                        self.dev_status, stream)
+        self._kept = (n, ac, scales)
+        return y
+
+    def backward(self, dy, wgrad: bool = True, stream=None):
+        """Gradients of the last forward_train(): dx, or with wgrad
+        (dx, dw13, dw2), all of the block's dtype; a norm's parameters'
+        gradients are left in norm.dweight and norm.dbias."""
+        import torch
+        if self._kept is None:
+            raise RuntimeError("backward() needs a forward_train() first")
+        n, ac, scales = self._kept
+        inter = self.w2.shape[1]
+        dx = torch.empty_like(dy)
+        dw13 = torch.empty_like(self.w13) if wgrad else None
+        dw2 = torch.empty_like(self.w2) if wgrad else None
+        moe_ffn_backward(dy, n, self.w13, self.w2, ac, scales, self._hidden(dy, 2 * inter),
+                         self._hidden(dy, inter), dx, dw13, dw2, self.dev_status, stream)
+        if self.norm is not None:
+            dx = self.norm.backward(dx, stream=stream)
+        return (dx, dw13, dw2) if wgrad else dx
+
+    def status(self, stream=None) -> int:
+        """Device status word (0 = fine); synchronises the stream."""
+        return moe_read_status(self.dev_status, stream)
 
 
 class MoeLayer:
@@ -51,10 +189,15 @@ class MoeLayer:
     """
 
     def __init__(self, shape: MoeShape, router_w, bias, device=None, host_io=False,
-                 scales: str = "fp32"):
+                 scales: str = "fp32", norm: Optional[LayerNorm] = None):
         """scales: "fp32" (the pages' recipe: FP32 scales, per-128-K promotion)
-        or "ue8m0" (power-of-two scales, block-scaled tensor-core GEMMs)."""
+        or "ue8m0" (power-of-two scales, block-scaled tensor-core GEMMs).
+        norm: a LayerNorm that forward, forward_train and backward put in
+        front of the layer."""
         import torch
+        if norm is not None and host_io:
+            raise ValueError("host-buffer calls take no norm")
+        self.norm = norm
         if scales not in ("fp32", "ue8m0"):
             raise ValueError("scales must be 'fp32' or 'ue8m0'")
         if scales == "ue8m0" and host_io:
@@ -114,6 +257,8 @@ class MoeLayer:
     def forward(self, x, y=None, update_bias: bool = False, logit_offset=None, stream=None):
         """y = MoE(x) for bf16 x [T, d] on the GPU; returns y (bf16 [T, d])."""
         import torch
+        if self.norm is not None:
+            x = self.norm.forward(x, stream=stream)
         if y is None:
             y = torch.empty_like(x)
         fwd = moe_layer_forward if self.scales == "fp32" else moe_layer_forward_mx
@@ -157,21 +302,34 @@ class MoeLayer:
                 "xs": torch.empty((d // 128, R), dtype=f32, device=dev),
                 "hq": torch.empty((R, I), dtype=u8, device=dev),
                 "hs": torch.empty((I // 128, R), dtype=f32, device=dev),
-                "o": torch.empty((R, d), dtype=f32, device=dev),
+                "o": None,  # fp32 [R, d], or (codes, scales) kept in 8 bits
+                "ac": None,  # gate and up kept in 8 bits: (codes, scales)
                 "x": None,
             }
         return self._train
 
     def forward_train(self, x, y=None, update_bias: bool = False, logit_offset=None,
-                      stream=None):
+                      stream=None, keep: Optional[str] = None):
         """The forward pass (fp32-scale recipe) through the stage entry points,
         keeping what backward() needs: the chosen affinities, the permuted FP8
         rows and the expert outputs.  y equals forward()'s bit for bit; x
-        must stay unchanged until backward() has run."""
+        must stay unchanged until backward() has run.
+
+        keep: None keeps the expert outputs in fp32 and lets backward()
+        recompute gate and up from the FP8 rows (one more W13 GEMM).  "fp8"
+        keeps both, and a norm's input, in 8 bits: a quarter of the outputs'
+        bytes, no recomputation, gradients from 8-bit values."""
         import torch
         if self.scales != "fp32":
             raise ValueError("the backward pass uses the fp32-scale layer")
+        if keep is not None and keep != "fp8":
+            raise ValueError("keep must be None or 'fp8'")
+        if self.norm is not None:
+            x = self.norm.forward_train(x, keep=keep or "full", stream=stream)
         sh, b = self.shape, self._train_buffers()
+        b["ac"] = None
+        if keep:
+            b["o"] = None
         N, d, I, K, T = sh.n_routed, sh.d, sh.inter, sh.topk, sh.T
         R = T * K + T
         if y is None:
@@ -182,13 +340,23 @@ class MoeLayer:
                          stream)
         moe_quant_permute(sh, x, self.topk_idx, self.expert_counts, b["xq"], b["xs"],
                           self.expert_offsets, self.row_of_pair, b["perm_ws"], st, stream)
-        moe_grouped_gemm_fp8(N + 1, self.expert_offsets, R, b["xq"], b["xs"], d, self.w13,
-                             self.w13_scales, 2 * I, MOE_EPI_SWIGLU_QUANT, b["hq"], b["hs"], st,
-                             stream)
+        if keep:
+            b["ac"] = (torch.empty((R, 2 * I), dtype=torch.uint8, device=self.device),
+                       torch.empty((2 * I // 128, R), dtype=torch.float32, device=self.device))
+            moe_grouped_gemm_fp8_ckpt(N + 1, self.expert_offsets, R, b["xq"], b["xs"], d,
+                                      self.w13, self.w13_scales, 2 * I, b["hq"], b["hs"],
+                                      *b["ac"], st, stream)
+        else:
+            moe_grouped_gemm_fp8(N + 1, self.expert_offsets, R, b["xq"], b["xs"], d, self.w13,
+                                 self.w13_scales, 2 * I, MOE_EPI_SWIGLU_QUANT, b["hq"], b["hs"],
+                                 st, stream)
+        # fp32 outputs: a buffer of the layer's, or (keep) until they are packed
+        o = b["o"] if not keep and torch.is_tensor(b["o"]) else torch.empty(
+            (R, d), dtype=torch.float32, device=self.device)
         moe_grouped_gemm_fp8(N + 1, self.expert_offsets, R, b["hq"], b["hs"], I, self.w2,
-                             self.w2_scales, d, MOE_EPI_F32, b["o"], None, st, stream)
-        moe_combine(sh, b["o"], self.expert_offsets, self.row_of_pair, self.topk_gate, y, st,
-                    stream)
+                             self.w2_scales, d, MOE_EPI_F32, o, None, st, stream)
+        moe_combine(sh, o, self.expert_offsets, self.row_of_pair, self.topk_gate, y, st, stream)
+        b["o"] = _pack(o, stream) if keep else o
         if update_bias:
             moe_update_bias(sh, self.expert_counts, self.bias, st, stream)
         b["x"] = x
@@ -228,6 +396,11 @@ class MoeLayer:
         tiles along the rows (x from the layer input, do = gate dy, h and
         [da | dc] from the recomputed fp32 a, c).
 
+        After forward_train(keep="fp8") a, c and the expert outputs are the
+        kept 8-bit values and nothing is recomputed.  With a norm, dx is the
+        gradient of the norm's input; its parameters' gradients are left in
+        norm.dweight and norm.dbias.
+
         marks: a list, or None; given a list, a timing CUDA event recorded on
         the stream after each stage is appended as (stage name, event), with
         ("start", event) first."""
@@ -259,13 +432,18 @@ class MoeLayer:
         moe_grouped_gemm_fp8(N + 1, off, R, do_q, do_s, d, w2t, w2t_s, I, MOE_EPI_F32, dh, None,
                              st, stream)
         mark("gemm_dh")
-        ac = torch.empty((R, 2 * I), dtype=f32, device=dev)
-        moe_grouped_gemm_fp8(N + 1, off, R, b["xq"], b["xs"], d, self.w13, self.w13_scales,
-                             2 * I, MOE_EPI_F32, ac, None, st, stream)
-        mark("gemm_ac_recompute")
+        kept = b["ac"] is not None
+        if not kept:
+            ac = torch.empty((R, 2 * I), dtype=f32, device=dev)
+            moe_grouped_gemm_fp8(N + 1, off, R, b["xq"], b["xs"], d, self.w13, self.w13_scales,
+                                 2 * I, MOE_EPI_F32, ac, None, st, stream)
+            mark("gemm_ac_recompute")
         gq = torch.empty((R, 2 * I), dtype=u8, device=dev)
         gs = torch.empty((2 * I // 128, R), dtype=f32, device=dev)
-        moe_swiglu_backward_quant(dh, ac, R, I, R, gq, gs, st, stream)
+        if kept:
+            moe_swiglu_backward_quant_ckpt(dh, *b["ac"], R, I, R, gq, gs, st, stream)
+        else:
+            moe_swiglu_backward_quant(dh, ac, R, I, R, gq, gs, st, stream)
         mark("swiglu_backward_quant")
         dx_rows = torch.empty((R, d), dtype=f32, device=dev)
         moe_grouped_gemm_fp8(N + 1, off, R, gq, gs, 2 * I, w13t, w13t_s, d, MOE_EPI_F32,
@@ -273,7 +451,11 @@ class MoeLayer:
         mark("gemm_dx")
         dgate = torch.empty((T, K), dtype=f32, device=dev)
         du = torch.empty((T, K), dtype=f32, device=dev)
-        moe_gate_backward(sh, dy, b["o"], self.row_of_pair, b["score"], dgate, du, st, stream)
+        if kept:
+            moe_gate_backward_ckpt(sh, dy, *b["o"], self.row_of_pair, b["score"], dgate, du, st,
+                                   stream)
+        else:
+            moe_gate_backward(sh, dy, b["o"], self.row_of_pair, b["score"], dgate, du, st, stream)
         mark("gate_backward")
         dx_router = torch.empty((T, d), dtype=f32, device=dev)
         d_router_w = torch.empty((N, d), dtype=f32, device=dev)
@@ -287,6 +469,9 @@ class MoeLayer:
         moe_dx_combine(sh, dx_rows, dx_router, self.row_of_pair, dx, st, stream)
         mark("dx_combine")
         self.last_dgate, self.last_du = dgate, du
+        if self.norm is not None:
+            dx = self.norm.backward(dx, stream=stream)
+            mark("norm_backward")
         if not wgrad:
             return dx, d_router_w
         # ---- weight gradients (pair_scratch holds the permutation's inverse)
@@ -302,7 +487,10 @@ class MoeLayer:
         dacts = torch.empty((nb, 2 * I), dtype=f32, device=dev)
         if T > 0:  # with no rows no group has K blocks: the operands are never read
             moe_wgrad_quant_x(sh, b["x"], pair_scratch, blocks, xt, xts, st, stream)
-            moe_wgrad_quant_dac(dh, ac, I, blocks, dact, dacts, st, stream)
+            if kept:
+                moe_wgrad_quant_dac_ckpt(dh, *b["ac"], I, blocks, dact, dacts, st, stream)
+            else:
+                moe_wgrad_quant_dac(dh, ac, I, blocks, dact, dacts, st, stream)
         mark("wgrad_quant_x_dac")
         dW13 = torch.empty((G, 2 * I, d), dtype=f32, device=dev)
         moe_grouped_gemm_wgrad(G, kb_off, nb, dact, dacts, 2 * I, xt, xts, d, dW13, st, stream)
@@ -315,7 +503,10 @@ class MoeLayer:
         if T > 0:
             moe_wgrad_quant_do(sh, dy, self.topk_gate, pair_scratch, blocks, dot, dots, st,
                                stream)
-            moe_wgrad_quant_h(ac, I, blocks, ht, hts, st, stream)
+            if kept:
+                moe_wgrad_quant_h_ckpt(*b["ac"], I, blocks, ht, hts, st, stream)
+            else:
+                moe_wgrad_quant_h(ac, I, blocks, ht, hts, st, stream)
         mark("wgrad_quant_do_h")
         dW2 = torch.empty((G, d, I), dtype=f32, device=dev)
         moe_grouped_gemm_wgrad(G, kb_off, nb, dot, dots, d, ht, hts, I, dW2, st, stream)

@@ -121,6 +121,7 @@ def lib() -> ctypes.CDLL:
             "moe_ckpt_row_bytes": (I64, [I64]),
             "moe_ckpt_pack": (I, [P, I, I64, I64, P, P, P, P]),
             "moe_ckpt_unpack": (I, [P, P, I64, I64, P, I, P, P]),
+            "moe_grouped_gemm_fp8_ckpt": (I, [I, P, I, P, P, I, P, P, I, P, P, P, P, P, P]),
             "moe_swiglu_backward_quant_ckpt": (I, [P, P, P, I64, I, I64, P, P, P, P]),
             "moe_wgrad_quant_h_ckpt": (I, [P, P, I64, I, P, I, P, P, P, P]),
             "moe_wgrad_quant_dac_ckpt": (I, [P, P, P, I64, I, P, I, P, P, P, P]),
@@ -703,6 +704,16 @@ def moe_ckpt_unpack(q, scales, y, dev_status=None, stream=None):
           ("scales", scales, (_tiles(cols), rows), _f32()))
     _check("moe_ckpt_unpack", lib().moe_ckpt_unpack(_ptr(q), _ptr(scales), rows, cols, _ptr(y), ty,
                                                     _ptr(dev_status), _stream(stream)))
+
+
+def moe_grouped_gemm_fp8_ckpt(n_groups, group_offsets, max_rows, a, a_scales, k, w, w_scales, n,
+                              out, out_scales, ac_q, ac_scales, dev_status=None, stream=None):
+    """moe_grouped_gemm_fp8 with MOE_EPI_SWIGLU_QUANT that also keeps gate and
+    up in 8 bits."""
+    _check("moe_grouped_gemm_fp8_ckpt", lib().moe_grouped_gemm_fp8_ckpt(
+        int(n_groups), _ptr(group_offsets), int(max_rows), _ptr(a), _ptr(a_scales), int(k),
+        _ptr(w), _ptr(w_scales), int(n), _ptr(out), _ptr(out_scales), _ptr(ac_q),
+        _ptr(ac_scales), _ptr(dev_status), _stream(stream)))
 
 
 def moe_swiglu_backward_quant_ckpt(dh, ac_q, ac_scales, rows, inter, rows_total, q, q_scales,

@@ -44,7 +44,7 @@
 #include <cstdlib>
 #include <mutex>
 
-#include "common.cuh"
+#include "elem.cuh"
 
 namespace moe {
 namespace {
@@ -115,6 +115,9 @@ struct GemmParams {
     const uint8_t* a_sf;     // [nkb, max_rows] scale bytes of the tokens' 1x128 tiles
     const uint8_t* w_sf;     // [n_groups, n/128, nkb] scale bytes of the weight blocks
     uint8_t* out_sf;         // SwiGLU: [n/256, max_rows] scale bytes of h
+    // SwiGLU that keeps gate and up for the backward pass (KEEP)
+    uint8_t* ac_q;           // [max_rows, n] codes: gate columns, then up columns
+    float* ac_scales;        // [n/128, max_rows]
 };
 
 // Token tensor maps, one per box height (128, 64, 32, 16 rows).
@@ -140,6 +143,7 @@ struct SharedState {
     alignas(16) float sa[kScaleSlots][kBM];   // token scales of one K block
     alignas(16) float sb[kScaleSlots][2];     // the two weight-block scales
     alignas(16) float red[2][2][kBM];         // [item parity][half][token] amax of h
+    alignas(16) float2 kept[2][2][kBM];       // the same of gate and up (KEEP)
 };
 
 template <bool PAIR, bool SWIGLU, bool WIDE>
@@ -865,6 +869,21 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const uint64_t (
     }
 }
 
+// 64 values -> 64 codes at q (16-byte aligned)
+__device__ __forceinline__ void put_codes64(uint8_t* q, const float* v, float inv) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float* f = v + 16 * i + 4 * j;
+            u[j] = e4m3x2(__fmul_rn(f[0], inv), __fmul_rn(f[1], inv)) |
+                   (uint32_t(e4m3x2(__fmul_rn(f[2], inv), __fmul_rn(f[3], inv))) << 16);
+        }
+        reinterpret_cast<uint4*>(q)[i] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+}
+
 // ================================================= promotion + epilogue (warps 4-11)
 // Thread (warp w, lane l) owns token row r = 32*(w%4) + l of its CTA's 128
 // and half h = (w-4)/4 of the partial's columns:
@@ -872,7 +891,8 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const uint64_t (
 //     (the same 64 features of W1 and W3);
 //   fp32 / bf16, C = 256: columns [128h, 128h+128) (weight block h);
 //   fp32 / bf16, C = 128: columns [64h, 64h+64) of the single weight block.
-template <bool PAIR, bool SWIGLU, bool WIDE>
+// KEEP (SwiGLU): gate and up, quantised in 1x128 tiles, are kept as well.
+template <bool PAIR, bool SWIGLU, bool WIDE, bool KEEP>
 __device__ __forceinline__ void promoter(const GemmParams& p, SharedState* ss, char* park_area,
                                          uint32_t tmem_base, const CUtensorMap* map_o, int rank,
                                          int unit, int units) {
@@ -979,6 +999,29 @@ __device__ __forceinline__ void promoter(const GemmParams& p, SharedState* ss, c
                 acc[2 * i] = f.x;
                 acc[2 * i + 1] = f.y;
             }
+            if constexpr (KEEP) {
+                float2 m = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    m.x = fmaxf(m.x, fabsf(acc[i]));
+                    m.y = fmaxf(m.y, fabsf(acc[64 + i]));
+                }
+                ss->kept[parity][half][r] = m;
+                named_bar(1, kPromoters * 32);
+                const float2 o = ss->kept[parity][half ^ 1][r];
+                float sg, ig, su, iu;
+                kept_scale(fmaxf(m.x, o.x), sg, ig);
+                kept_scale(fmaxf(m.y, o.y), su, iu);
+                if (row_ok) {
+                    uint8_t* q = p.ac_q + row * p.n + size_t(w.f) * 128 + half * 64;
+                    put_codes64(q, acc, ig);
+                    put_codes64(q + p.n / 2, acc + 64, iu);
+                    if (half == 0) {
+                        p.ac_scales[size_t(w.f) * p.max_rows + row] = sg;
+                        p.ac_scales[(size_t(p.n / 256) + w.f) * p.max_rows + row] = su;
+                    }
+                }
+            }
             float amax = 0.0f;
 #pragma unroll
             for (int i = 0; i < 64; ++i) {
@@ -1023,7 +1066,7 @@ __device__ __forceinline__ void promoter(const GemmParams& p, SharedState* ss, c
 }
 
 // ----------------------------------------------------------------- kernel
-template <bool PAIR, bool SWIGLU, bool WIDE>
+template <bool PAIR, bool SWIGLU, bool WIDE, bool KEEP = false>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
                         const __grid_constant__ AMaps maps_a,
@@ -1128,8 +1171,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (warp == 2) scale_loader<PAIR, SWIGLU, WIDE>(p, ss, rank, unit, units);
     } else {
         set_max_regs_inc<208>();
-        promoter<PAIR, SWIGLU, WIDE>(p, ss, reinterpret_cast<char*>(smem + C::kRingBytes), tmem_base,
-                               &map_o, rank, unit, units);
+        promoter<PAIR, SWIGLU, WIDE, KEEP>(p, ss, reinterpret_cast<char*>(smem + C::kRingBytes),
+                                           tmem_base, &map_o, rank, unit, units);
     }
 
     __syncthreads();
@@ -1586,16 +1629,16 @@ int pair_units() {
     return cache[dev];
 }
 
-template <bool PAIR, bool SWIGLU, bool WIDE>
+template <bool PAIR, bool SWIGLU, bool WIDE, bool KEEP = false>
 int launch(const GemmParams& p, const CUtensorMap& mw, const AMaps& ma, const CUtensorMap& mo,
            int units, cudaStream_t st) {
-    if (cudaFuncSetAttribute(grouped_gemm_kernel<PAIR, SWIGLU, WIDE>,
+    if (cudaFuncSetAttribute(grouped_gemm_kernel<PAIR, SWIGLU, WIDE, KEEP>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(smem_bytes<PAIR, SWIGLU, WIDE>())) != cudaSuccess)
         return MOE_ERR_CUDA;
     if (!PAIR) {
-        grouped_gemm_kernel<PAIR, SWIGLU, WIDE><<<sm_count(), kThreads, smem_bytes<PAIR, SWIGLU, WIDE>(), st>>>(
-            mw, ma, mo, p);
+        grouped_gemm_kernel<PAIR, SWIGLU, WIDE, KEEP>
+            <<<sm_count(), kThreads, smem_bytes<PAIR, SWIGLU, WIDE>(), st>>>(mw, ma, mo, p);
         return check_launch();
     }
     cudaLaunchConfig_t cfg = {};
@@ -1610,7 +1653,8 @@ int launch(const GemmParams& p, const CUtensorMap& mw, const AMaps& ma, const CU
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<PAIR, SWIGLU, WIDE>, mw, ma, mo, p) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<PAIR, SWIGLU, WIDE, KEEP>, mw, ma, mo, p) !=
+        cudaSuccess)
         return MOE_ERR_CUDA;
     return check_launch();
 }
@@ -2063,7 +2107,8 @@ namespace moe {
 int grouped_gemm_fp8(int n_groups, const int32_t* group_offsets, int max_rows, const uint8_t* a,
                      const float* a_scales, int k, const uint8_t* w, const float* w_scales, int n,
                      int epilogue, void* out, float* out_scales, const int32_t* group_weight,
-                     int n_weights, int* dev_status, void* stream);
+                     int n_weights, uint8_t* ac_q, float* ac_scales, int* dev_status,
+                     void* stream);
 }
 
 extern "C" MOE_API int moe_grouped_gemm_fp8(int n_groups, const int32_t* group_offsets,
@@ -2073,7 +2118,22 @@ extern "C" MOE_API int moe_grouped_gemm_fp8(int n_groups, const int32_t* group_o
                                             void* out, float* out_scales, int* dev_status,
                                             void* stream) {
     return grouped_gemm_fp8(n_groups, group_offsets, max_rows, a, a_scales, k, w, w_scales, n,
-                            epilogue, out, out_scales, nullptr, n_groups, dev_status, stream);
+                            epilogue, out, out_scales, nullptr, n_groups, nullptr, nullptr,
+                            dev_status, stream);
+}
+
+extern "C" MOE_API int moe_grouped_gemm_fp8_ckpt(int n_groups, const int32_t* group_offsets,
+                                                 int max_rows, const uint8_t* a,
+                                                 const float* a_scales, int k, const uint8_t* w,
+                                                 const float* w_scales, int n, uint8_t* out,
+                                                 float* out_scales, uint8_t* ac_q,
+                                                 float* ac_scales, int* dev_status,
+                                                 void* stream) {
+    if (max_rows != 0 && (!ac_q || !ac_scales)) return MOE_ERR_NULL;
+    if (!aligned16(ac_q)) return MOE_ERR_ALIGN;
+    return grouped_gemm_fp8(n_groups, group_offsets, max_rows, a, a_scales, k, w, w_scales, n,
+                            MOE_EPI_SWIGLU_QUANT, out, out_scales, nullptr, n_groups, ac_q,
+                            ac_scales, dev_status, stream);
 }
 
 extern "C" MOE_API int moe_grouped_gemm_fp8_indexed(
@@ -2084,14 +2144,15 @@ extern "C" MOE_API int moe_grouped_gemm_fp8_indexed(
     if (!group_weight) return MOE_ERR_NULL;
     if (n_weights < 1) return MOE_ERR_SHAPE;
     return grouped_gemm_fp8(n_groups, group_offsets, max_rows, a, a_scales, k, w, w_scales, n,
-                            epilogue, out, out_scales, group_weight, n_weights, dev_status, stream);
+                            epilogue, out, out_scales, group_weight, n_weights, nullptr, nullptr,
+                            dev_status, stream);
 }
 
 int moe::grouped_gemm_fp8(int n_groups, const int32_t* group_offsets, int max_rows,
                           const uint8_t* a, const float* a_scales, int k, const uint8_t* w,
                           const float* w_scales, int n, int epilogue, void* out,
                           float* out_scales, const int32_t* group_weight, int n_weights,
-                          int* dev_status, void* stream) {
+                          uint8_t* ac_q, float* ac_scales, int* dev_status, void* stream) {
     if (n_groups < 1 || n_groups > kMaxGroups || max_rows < 0 || k <= 0 || k % 128 || n <= 0 ||
         n % 128)
         return MOE_ERR_SHAPE;
@@ -2107,7 +2168,8 @@ int moe::grouped_gemm_fp8(int n_groups, const int32_t* group_offsets, int max_ro
     if (!device_is_sm100()) return MOE_ERR_DEVICE;
 
     const bool swiglu = epilogue == MOE_EPI_SWIGLU_QUANT;
-    const int units = gemm_pair_units(n_groups, max_rows, n, swiglu);
+    // (single CTAs wherever gate and up are kept)
+    const int units = ac_q ? 0 : gemm_pair_units(n_groups, max_rows, n, swiglu);
     const bool pair = units > 0;
 
     GemmParams p;
@@ -2131,6 +2193,8 @@ int moe::grouped_gemm_fp8(int n_groups, const int32_t* group_offsets, int max_ro
     p.fault = fault_injection();
     p.group_weight = group_weight;
     p.n_weights = n_weights;
+    p.ac_q = ac_q;
+    p.ac_scales = ac_scales;
 
     CUtensorMap mw, mo;
     AMaps ma;
@@ -2145,7 +2209,9 @@ int moe::grouped_gemm_fp8(int n_groups, const int32_t* group_offsets, int max_ro
     if (pair)
         return swiglu ? launch<true, true, true>(p, mw, ma, mo, units, st)
                       : launch<true, false, true>(p, mw, ma, mo, units, st);
-    if (swiglu) return launch<false, true, true>(p, mw, ma, mo, 0, st);
+    if (swiglu)
+        return ac_q ? launch<false, true, true, true>(p, mw, ma, mo, 0, st)
+                    : launch<false, true, true>(p, mw, ma, mo, 0, st);
     return wide ? launch<false, false, true>(p, mw, ma, mo, 0, st)
                 : launch<false, false, false>(p, mw, ma, mo, 0, st);
 }

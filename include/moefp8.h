@@ -801,6 +801,11 @@ MOE_API int moe_layernorm_backward(const void* dy, int type, const void* x, int 
  *   16-byte aligned x.
  * moe_ckpt_unpack: y = type(fp32(code scale)).
  *
+ * moe_grouped_gemm_fp8_ckpt: moe_grouped_gemm_fp8 with MOE_EPI_SWIGLU_QUANT
+ *   (out, out_scales the same bits) that also keeps gate and up from its
+ *   accumulators: ac_q uint8 [max_rows, n], ac_scales fp32 [n / 128,
+ *   max_rows], rows outside every group not written.
+ *
  * The backward steps that read a checkpoint where it lies:
  * moe_swiglu_backward_quant_ckpt: moe_swiglu_backward_quant with [a | c] kept
  *   as ac_q (uint8 [rows, 2 inter]) and ac_scales (fp32 [2 inter / 128,
@@ -816,6 +821,11 @@ MOE_API int moe_ckpt_pack(const void* x, int type, int64_t rows, int64_t cols, u
                           float* scales, int* dev_status, void* stream);
 MOE_API int moe_ckpt_unpack(const uint8_t* q, const float* scales, int64_t rows, int64_t cols,
                             void* y, int type, int* dev_status, void* stream);
+MOE_API int moe_grouped_gemm_fp8_ckpt(int n_groups, const int32_t* group_offsets, int max_rows,
+                                      const uint8_t* a, const float* a_scales, int k,
+                                      const uint8_t* w, const float* w_scales, int n,
+                                      uint8_t* out, float* out_scales, uint8_t* ac_q,
+                                      float* ac_scales, int* dev_status, void* stream);
 MOE_API int moe_swiglu_backward_quant_ckpt(const float* dh, const uint8_t* ac_q,
                                            const float* ac_scales, int64_t rows, int inter,
                                            int64_t rows_total, uint8_t* q, float* q_scales,

@@ -67,6 +67,10 @@ def test_checkpoint_refusals(moe):
     assert L.moe_wgrad_quant_h_ckpt(None, A, 4, 128, A, 1, A, A, None, None) == NULL
     assert L.moe_wgrad_quant_dac_ckpt(A, A, None, 4, 128, A, 1, A, A, None, None) == NULL
     assert L.moe_wgrad_quant_dac_ckpt(A, A + 8, A, 4, 128, A, 1, A, A, None, None) == ALIGN
+    def gemm(out=A, os=A, q=A, s=A, n=256, rows=8):
+        return L.moe_grouped_gemm_fp8_ckpt(1, A, rows, A, A, 128, A, A, n, out, os, q, s, None, None)
+    assert gemm(q=None) == NULL and gemm(s=None) == NULL and gemm(os=None) == NULL
+    assert gemm(q=A + 8) == ALIGN and gemm(n=384) == SHAPE and gemm(rows=0, q=None, s=None) == 0
     sh = moe.make_shape(4, 128, 8, 1, 1, 2, 128)
     assert L.moe_gate_backward_ckpt(ctypes.byref(sh), A, A, None, A, A, A, A, None, None) == NULL
     assert L.moe_gate_backward_ckpt(ctypes.byref(sh), A, A + 8, A, A, A, A, A, None, None) == ALIGN
