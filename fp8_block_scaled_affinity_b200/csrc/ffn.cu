@@ -90,6 +90,7 @@ struct Args {
     int64_t rows;            // tokens
     void* ac;                // kept a, c
     float* ac_scales;
+    int wait_first;          // 1: operands come from the kernel before this one
     int* dev_status;
     uint64_t wait_limit_ns;
 };
@@ -144,57 +145,60 @@ __device__ __forceinline__ Tile decode_for(const Args& a, int t) {
     return decode(a, t, EPI == kGated ? 128 : 0);
 }
 
-// ------------------------------------------------ TMA producer (warp 0)
-template <int EPI>
+// ------------------------------------------------ TMA producers (warps 0 and 2)
+// Warp 0 loads A and announces the stage's bytes, warp 2 loads B.
+template <int EPI, bool IS_A>
 __device__ __forceinline__ void producer(const Args& a, uint8_t* smem, Shared* ss, int rank,
                                          int unit, int units) {
-    if ((threadIdx.x & 31) == 0) {
-        uint32_t it = 0, issued = 0, issued_parity = 0;
-        bool ok = true;
-        for (int t = unit; ok && t < a.tiles; t += units) {
-            const Tile w = decode_for<EPI>(a, t);
-            const Problem& p = a.p[w.p];
-            const int half = p.nt / 2;
-            const int am = w.m0 + 128 * rank;
-            // this CTA's rows of B: half the tile's columns, or 128 rows of
-            // W1 (rank 0) and of W3 (rank 1)
-            const int bn = EPI == kGated ? w.n0 + rank * a.inter : w.n0 + rank * half;
-            const int b_pieces = (half + 63) / 64;
-            const uint32_t b_bytes = p.b_mn ? b_pieces * kPieceBytes : half * 128;
-            const uint32_t tx = 2 * (kOperandBytes + b_bytes);
-            for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-                const int s = it % kStages;
-                const uint32_t par = (it / kStages) & 1u;
-                ok = pair_wait(smem_u32(&ss->empty[s]), par ^ 1u, &ss->ps, a.dev_status);
-                if (!ok) break;
-                const uint32_t sa = smem_u32(smem + size_t(s) * kStageBytes);
-                const uint32_t sb = sa + kOperandBytes;
-                const uint32_t local = smem_u32(&ss->full[s]);
-                const uint32_t bar = mapa(local, 0);
-                const int k0 = kb * kTileK;
-                if (rank == 0) mbar_arrive_expect_tx(local, tx);
-                if (p.a_mn) {
-                    pair_tma_load_2d(sa, &p.a, bar, am, k0);
-                    pair_tma_load_2d(sa + kPieceBytes, &p.a, bar, am + 64, k0);
+    const bool lead = elect_one();
+    // the leader's barrier of stage 0
+    const uint32_t bar0 = uniform(mapa(smem_u32(&ss->full[0]), 0));
+    uint32_t s = 0, par = 1, issued = 0, issued_parity = 0;
+    bool ok = true;
+    for (int t = unit; ok && t < a.tiles; t += units) {
+        const Tile w = decode_for<EPI>(a, t);
+        const Problem& p = a.p[w.p];
+        const int half = p.nt / 2;
+        // this CTA's rows of A; and of B: half the tile's columns, or 128
+        // rows of W1 (rank 0) and of W3 (rank 1)
+        const int first =
+            IS_A ? w.m0 + 128 * rank : w.n0 + rank * (EPI == kGated ? a.inter : half);
+        const CUtensorMap* map = IS_A ? &p.a : &p.b;
+        const int mn = IS_A ? p.a_mn : p.b_mn;
+        const int b_pieces = (half + 63) / 64;
+        const int pieces = IS_A ? 2 : b_pieces;
+        const uint32_t tx = 2 * (kOperandBytes + (p.b_mn ? b_pieces * kPieceBytes : half * 128));
+        const int nkb = p.nkb;
+        for (int kb = 0; kb < nkb; ++kb) {
+            ok = pair_wait(smem_u32(&ss->empty[s]), par, &ss->ps, a.dev_status);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            const uint32_t dst =
+                smem_u32(smem) + s * uint32_t(kStageBytes) + (IS_A ? 0u : uint32_t(kOperandBytes));
+            const uint32_t bar = bar0 + 8 * s;
+            const int k0 = kb * kTileK;
+            if (lead) {
+                if (IS_A && rank == 0) mbar_arrive_expect_tx(smem_u32(&ss->full[s]), tx);
+                if (mn) {
+                    pair_tma_load_2d(dst, map, bar, first, k0);
+                    if (pieces > 1) pair_tma_load_2d(dst + kPieceBytes, map, bar, first + 64, k0);
                 } else {
-                    pair_tma_load_2d(sa, &p.a, bar, k0, am);
+                    pair_tma_load_2d(dst, map, bar, k0, first);
                 }
-                if (p.b_mn) {
-                    for (int i = 0; i < b_pieces; ++i)
-                        pair_tma_load_2d(sb + i * kPieceBytes, &p.b, bar, bn + 64 * i, k0);
-                } else {
-                    pair_tma_load_2d(sb, &p.b, bar, k0, bn);
-                }
-                issued |= 1u << s;
-                issued_parity = (issued_parity & ~(1u << s)) | (par << s);
+            }
+            issued |= 1u << s;
+            issued_parity = (issued_parity & ~(1u << s)) | ((par ^ 1u) << s);
+            if (++s == kStages) {
+                s = 0;
+                par ^= 1u;
             }
         }
-        if (!ok && rank == 0)  // loads in flight land before the CTA leaves
-            for (int s = 0; s < kStages; ++s)
-                if ((issued >> s) & 1u)
-                    mbar_quiesce(smem_u32(&ss->full[s]), (issued_parity >> s) & 1u, nullptr,
-                                 ss->ps.wait_limit);
     }
+    if (!ok && rank == 0 && IS_A && lead)  // loads in flight land before the CTA leaves
+        for (int i = 0; i < kStages; ++i)
+            if ((issued >> i) & 1u)
+                mbar_quiesce(smem_u32(&ss->full[i]), (issued_parity >> i) & 1u, nullptr,
+                             ss->ps.wait_limit);
     __syncwarp();
 }
 
@@ -202,40 +206,47 @@ __device__ __forceinline__ void producer(const Args& a, uint8_t* smem, Shared* s
 template <int EPI, bool BF16>
 __device__ __forceinline__ void issuer(const Args& a, uint8_t* smem, Shared* ss,
                                        uint32_t tmem_base, int unit, int units) {
-    if ((threadIdx.x & 31) == 0) {
-        uint32_t it = 0, n = 0;
-        bool ok = true;
-        for (int t = unit; ok && t < a.tiles; t += units, ++n) {
-            const Tile w = decode_for<EPI>(a, t);
-            const Problem& p = a.p[w.p];
-            const uint32_t idesc = idesc_f16(BF16, p.a_mn, p.b_mn, kTileM, p.nt);
-            // bytes per 16 K elements, in descriptor units of 16
-            const uint32_t a_step = p.a_mn ? 2048 / 16 : 32 / 16;
-            const uint32_t b_step = p.b_mn ? 2048 / 16 : 32 / 16;
-            const uint32_t d = tmem_base + (n & 1) * 256;
-            ok = pair_wait(smem_u32(&ss->tempty[n & 1]), ((n >> 1) & 1u) ^ 1u, &ss->ps,
-                           a.dev_status);
+    const bool lead = elect_one();
+    uint32_t s = 0, par = 0, n = 0;
+    bool ok = true;
+    const uint64_t desc0 = sw128_desc16(smem_u32(smem), kPieceBytes);
+    for (int t = unit; ok && t < a.tiles; t += units, ++n) {
+        const Tile w = decode_for<EPI>(a, t);
+        const Problem& p = a.p[w.p];
+        const uint32_t idesc = idesc_f16(BF16, p.a_mn, p.b_mn, kTileM, p.nt);
+        // bytes per 16 K elements, in descriptor units of 16
+        const uint32_t a_step = p.a_mn ? 2048 / 16 : 32 / 16;
+        const uint32_t b_step = p.b_mn ? 2048 / 16 : 32 / 16;
+        const uint32_t d = tmem_base + (n & 1) * 256;
+        const int nkb = p.nkb;
+        ok = pair_wait(smem_u32(&ss->tempty[n & 1]), ((n >> 1) & 1u) ^ 1u, &ss->ps, a.dev_status);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        fence_after();
+        for (int kb = 0; kb < nkb; ++kb) {
+            ok = pair_wait(smem_u32(&ss->full[s]), par, &ss->ps, a.dev_status);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             fence_after();
-            for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-                const int s = it % kStages;
-                ok = pair_wait(smem_u32(&ss->full[s]), (it / kStages) & 1u, &ss->ps,
-                               a.dev_status);
-                if (!ok) break;
-                fence_after();
-                const uint32_t sa = smem_u32(smem + size_t(s) * kStageBytes);
-                uint64_t ad = sw128_desc16(sa, kPieceBytes);
-                uint64_t bd = sw128_desc16(sa + kOperandBytes, kPieceBytes);
+            const uint64_t ad = desc0 + s * uint32_t(kStageBytes / 16);
+            const uint64_t bd = ad + kOperandBytes / 16;
+            if (lead) {
 #pragma unroll
-                for (int kk = 0; kk < kTileK / 16; ++kk) {
-                    pair_mma_f16(d, ad, bd, idesc, (kb | kk) ? 1u : 0u);
-                    ad += a_step;
-                    bd += b_step;
-                }
+                for (int kk = 0; kk < kTileK / 16; ++kk)
+                    pair_mma_f16(d, ad + kk * a_step, bd + kk * b_step, idesc,
+                                 (kb | kk) ? 1u : 0u);
                 pair_commit_both(smem_u32(&ss->empty[s]));
             }
-            if (ok) pair_commit_both(smem_u32(&ss->tfull[n & 1]));
+            __syncwarp();
+            if (++s == kStages) {
+                s = 0;
+                par ^= 1u;
+            }
         }
+        if (ok && lead) pair_commit_both(smem_u32(&ss->tfull[n & 1]));
+        __syncwarp();
+    }
+    if (lead) {
         // every MMA has completed once this fires (after an abort too)
         pair_commit(smem_u32(&ss->drain));
         mbar_quiesce(smem_u32(&ss->drain), 0, nullptr, ss->ps.wait_limit);
@@ -490,8 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
     char* park = reinterpret_cast<char*>(smem + kStages * kStageBytes);
     float* red = reinterpret_cast<float*>(park + Cfg<EPI>::kParkBytes);
     Shared* ss = reinterpret_cast<Shared*>(park + Cfg<EPI>::kParkBytes + Cfg<EPI>::kRedBytes);
-    const int warp = threadIdx.x >> 5;
-    const int rank = int(cluster_rank());
+    const int warp = int(uniform(threadIdx.x >> 5));
+    const int rank = int(blockIdx.x & 1);  // clusters are pairs along x
     const int unit = int(blockIdx.x >> 1), units = int(gridDim.x >> 1);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -513,9 +524,15 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
     __syncthreads();
     cluster_sync();  // the peer's barriers exist before anyone signals them
     fence_after();
-    const uint32_t tmem_base = ss->tmem_base;
+    // The next launch may set itself up as this one's CTAs leave; its loads
+    // and stores wait for this grid's end.
+    launch_dependents();
+    if (a.wait_first) wait_dependencies();
+    const uint32_t tmem_base = uniform(ss->tmem_base);
     if (warp == 0)
-        producer<EPI>(a, smem, ss, rank, unit, units);
+        producer<EPI, true>(a, smem, ss, rank, unit, units);
+    else if (warp == 2)
+        producer<EPI, false>(a, smem, ss, rank, unit, units);
     else if (warp == 1 && rank == 0)
         issuer<EPI, std::is_same<T, bf16_t>::value>(a, smem, ss, tmem_base, unit, units);
     else if (warp >= 4)
@@ -639,7 +656,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     FewShared* ss = reinterpret_cast<FewShared*>(smem + a.ring);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = int(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int rank = blockIdx.x, split = gridDim.x;  // the cluster is the x row of the grid
     const int wt = blockIdx.y;
     const int64_t t0 = int64_t(blockIdx.z) * a.nt;
@@ -661,60 +678,80 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     __syncthreads();
     fence_after();
     launch_dependents();
-    const uint32_t tmem = ss->tmem_base;
+    const uint32_t tmem = uniform(ss->tmem_base);
     const int stage_bytes = kOperandBytes + a.nt * 128;
     bool ok = true;
     if (warp == 0) {
-        if (lane == 0) {
-            const int w0 = wt * (GATED ? 64 : 128);
-            auto load_w = [&](int i) {
-                const int s = i % a.stages, k0 = (kb0 + i) * kTileK;
-                const uint32_t bar = smem_u32(&ss->full[s]);
-                const uint32_t dst = smem_u32(smem + size_t(s) * stage_bytes);
-                mbar_arrive_expect_tx(bar, uint32_t(stage_bytes));
-                tma_load_2d(dst, &a.w, bar, k0, w0);
-                if (GATED) tma_load_2d(dst + kOperandBytes / 2, &a.w, bar, k0, a.w3 + w0);
-            };
-            auto load_x = [&](int i) {
-                const int s = i % a.stages;
-                tma_load_2d(smem_u32(smem + size_t(s) * stage_bytes) + kOperandBytes, &a.x,
-                            smem_u32(&ss->full[s]), (kb0 + i) * kTileK, int(t0));
-            };
-            // the first stages: weights before the wait, tokens after it
-            const int first = min(n, a.stages);
-            for (int i = 0; i < first; ++i) load_w(i);
-            if (a.wait_first) wait_dependencies();
-            for (int i = 0; i < first; ++i) load_x(i);
-            int i = first;
-            for (; i < n; ++i) {
-                ok = mbar_wait(smem_u32(&ss->empty[i % a.stages]), ((i / a.stages) & 1u) ^ 1u,
-                               &ss->abort_flag, a.dev_status, a.wait_limit_ns);
-                if (!ok) break;
-                load_w(i);
-                load_x(i);
+        const bool lead = elect_one();
+        const int w0 = wt * (GATED ? 64 : 128);
+        auto load_w = [&](int i, int s) {
+            const int k0 = (kb0 + i) * kTileK;
+            const uint32_t bar = smem_u32(&ss->full[s]);
+            const uint32_t dst = smem_u32(smem) + s * stage_bytes;
+            mbar_arrive_expect_tx(bar, uint32_t(stage_bytes));
+            tma_load_2d(dst, &a.w, bar, k0, w0);
+            if (GATED) tma_load_2d(dst + kOperandBytes / 2, &a.w, bar, k0, a.w3 + w0);
+        };
+        auto load_x = [&](int i, int s) {
+            tma_load_2d(smem_u32(smem) + s * stage_bytes + kOperandBytes, &a.x,
+                        smem_u32(&ss->full[s]), (kb0 + i) * kTileK, int(t0));
+        };
+        // the first stages: weights before the wait, tokens after it
+        const int first = min(n, a.stages);
+        if (lead)
+            for (int i = 0; i < first; ++i) load_w(i, i);
+        if (a.wait_first) wait_dependencies();
+        if (lead)
+            for (int i = 0; i < first; ++i) load_x(i, i);
+        __syncwarp();
+        int i = first, s = 0;
+        uint32_t par = 0;
+        for (; i < n; ++i) {
+            ok = mbar_wait(smem_u32(&ss->empty[s]), par, &ss->abort_flag, a.dev_status,
+                           a.wait_limit_ns);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            if (lead) {
+                load_w(i, s);
+                load_x(i, s);
             }
-            if (!ok)  // loads in flight land before the CTA leaves
-                for (int j = max(0, i - a.stages); j < i; ++j)
-                    mbar_quiesce(smem_u32(&ss->full[j % a.stages]), (j / a.stages) & 1u, nullptr,
-                                 a.wait_limit_ns);
+            __syncwarp();
+            if (++s == a.stages) {
+                s = 0;
+                par ^= 1u;
+            }
         }
+        if (!ok && lead)  // loads in flight land before the CTA leaves
+            for (int j = max(0, i - a.stages); j < i; ++j)
+                mbar_quiesce(smem_u32(&ss->full[j % a.stages]), (j / a.stages) & 1u, nullptr,
+                             a.wait_limit_ns);
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc =
-                idesc_f16(std::is_same<T, bf16_t>::value, 0, 0, 128, a.nt);
-            for (int i = 0; i < n; ++i) {
-                const int s = i % a.stages;
-                ok = mbar_wait(smem_u32(&ss->full[s]), (i / a.stages) & 1u, &ss->abort_flag,
-                               a.dev_status, a.wait_limit_ns);
-                if (!ok) break;
-                fence_after();
-                const uint32_t sa = smem_u32(smem + size_t(s) * stage_bytes);
-                uint64_t ad = sw128_desc16(sa, 16), bd = sw128_desc16(sa + kOperandBytes, 16);
+        const bool lead = elect_one();
+        const uint32_t idesc = idesc_f16(std::is_same<T, bf16_t>::value, 0, 0, 128, a.nt);
+        const uint64_t desc0 = sw128_desc16(smem_u32(smem), 16);
+        int s = 0;
+        uint32_t par = 0;
+        for (int i = 0; i < n; ++i) {
+            ok = mbar_wait(smem_u32(&ss->full[s]), par, &ss->abort_flag, a.dev_status,
+                           a.wait_limit_ns);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            fence_after();
+            const uint64_t ad = desc0 + uint32_t(s * (stage_bytes / 16));
+            const uint64_t bd = ad + kOperandBytes / 16;
+            if (lead) {
 #pragma unroll
-                for (int kk = 0; kk < kTileK / 16; ++kk, ad += 2, bd += 2)
-                    mma_f16(tmem, ad, bd, idesc, (i | kk) ? 1u : 0u);
+                for (int kk = 0; kk < kTileK / 16; ++kk)
+                    mma_f16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (i | kk) ? 1u : 0u);
                 commit(smem_u32(&ss->empty[s]));
             }
+            __syncwarp();
+            if (++s == a.stages) {
+                s = 0;
+                par ^= 1u;
+            }
+        }
+        if (lead) {
             commit(smem_u32(&ss->done));
             mbar_quiesce(smem_u32(&ss->done), 0, nullptr, a.wait_limit_ns);
         }
@@ -884,15 +921,18 @@ int launch(Args& a, cudaStream_t st) {
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = Cfg<EPI>::kSmem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const int units = pair_units<EPI, KEPT, T>(cfg);
     if (units < 1) return MOE_ERR_CUDA;
+    if (a.wait_first) cfg.numAttrs = 2;
     cfg.gridDim = dim3(unsigned(2 * std::min(units, a.tiles)), 1, 1);
     if (cudaLaunchKernelEx(&cfg, ffn_kernel<EPI, KEPT, T>, a) != cudaSuccess) return MOE_ERR_CUDA;
     return check_launch();
@@ -916,6 +956,28 @@ struct Maker {
                                CU_TENSOR_MAP_L2_PROMOTION_NONE);
     }
 };
+
+// Columns of the pair tiles of an m x n product with a K-major B: the width
+// that gives the shortest run over the device's pairs, a tile costing its
+// columns and about 64 more (filling the pipeline, its epilogue).  4096 x 7168
+// on 74 pairs: 7 rounds of 256 columns, or 7 of 224 (85 -> 80 us).  An MN-major
+// B comes in pieces of 64 columns for each half tile, so other widths load
+// what they do not use: 256 there (dy W2 in 13 tiles of 160 columns instead of
+// 8: 95 -> 110 us).
+int tile_width(int64_t m, int64_t n) {
+    const int pairs = std::max(1, sm_count() / 2);
+    int best = 256;
+    int64_t best_cost = INT64_MAX;
+    for (int nt = 256; nt >= 128; nt -= 32) {
+        const int64_t tiles = (m + kTileM - 1) / kTileM * ((n + nt - 1) / nt);
+        const int64_t cost = (tiles + pairs - 1) / pairs * (nt + 64);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = nt;
+        }
+    }
+    return best;
+}
 
 // out [m, n] = A B^T over k: A is [m, k] in memory, or [k, m] (a_mn); B is
 // [n, k], or [k, n] (b_mn).
@@ -963,6 +1025,7 @@ int backward(Maker mk, const void* dy, const void* x, const void* w13, const voi
     if (dx) product(b, mk, dac, false, w13, true, dx, rows, d, 2 * int64_t(I), 256);
     if (dw13) product(b, mk, dac, true, x, true, dw13, 2 * int64_t(I), d, rows, 256);
     if (dw2) product(b, mk, dy, true, h, true, dw2, d, I, rows, 256);
+    b.wait_first = 1;
     if (!mk.ok) return MOE_ERR_CUDA;
     const int rc = kept == kKept8 ? launch<kBackward, kKept8, T>(a, st)
                                   : launch<kBackward, kKept16, T>(a, st);
@@ -1118,7 +1181,8 @@ int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t ro
         mk.output(&a.o2, static_cast<uint16_t*>(ac) + I, rows, I, 2 * int64_t(I));
     }
     Args b = make_args(rows, I, dev_status);
-    product(b, mk, h, false, w2, false, y, rows, d, I, 256);
+    product(b, mk, h, false, w2, false, y, rows, d, I, tile_width(rows, d));
+    b.wait_first = 1;
     if (!mk.ok) return MOE_ERR_CUDA;
     if (!few_a) {
         rc = kept == kKept8    ? launch<kGated, kKept8, T>(a, st)
@@ -1126,7 +1190,7 @@ int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t ro
                                : launch<kGated, kKeptNone, T>(a, st);
         if (rc != MOE_OK) return rc;
     }
-    return few_b ? launch_few<false, T>(mk, fb, w2, h, y, rows, d, I, dev_status, false, st)
+    return few_b ? launch_few<false, T>(mk, fb, w2, h, y, rows, d, I, dev_status, true, st)
                  : launch<kPlain, kKeptNone, T>(b, st);
 }
 

@@ -15,6 +15,24 @@ struct PairState {
     uint32_t peer_abort;  // cluster address of the peer's abort_flag
 };
 
+// One lane of the (converged) warp.  The loops of the producers and the MMA
+// issuer run on whole warps and only their copies, MMAs and commits on this
+// lane: those instructions take their operands from uniform registers, and in
+// a loop that one lane runs alone every operand of every instruction is moved
+// there first (the dense block's 4096-token backward pass: 722 us; 539 us with
+// two such producers; see ffn.cu).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+// A value that is the same in all lanes, known as such to the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
