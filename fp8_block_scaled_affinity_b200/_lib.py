@@ -164,8 +164,8 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        c = _get_torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -602,35 +602,48 @@ def _mat(name, t, shape, dtype=None):
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
 
 
-def _mats(first, *specs) -> int:
+def _mats(first, *specs):
     """_mat for (name, tensor, shape, dtype) of a whole call, in the few
     attribute reads that a call of some microseconds can afford: the first
     tensor's device is compared with the current one, the others' with its.
-    Returns the device index."""
+    Returns the tensors' addresses (None for None)."""
     name, t, shape, dtype = first
     dev = t.get_device()
     if dev < 0 or dev != _current_device() or t.shape != shape or not t.is_contiguous():
         _mat(name, t, shape, dtype)
+    at = [t.data_ptr()]
     for name, t, shape, dtype in specs:
-        if t is not None and (t.get_device() != dev or t.dtype is not dtype or t.shape != shape
-                              or not t.is_contiguous()):
+        if t is None:
+            at.append(None)
+            continue
+        if (t.get_device() != dev or t.dtype is not dtype or t.shape != shape
+                or not t.is_contiguous()):
             _mat(name, t, shape, dtype)
-    return dev
+        at.append(t.data_ptr())
+    return at
 
 
 def _current_device() -> int:
-    import torch
-    return torch._C._cuda_getDevice()
+    return _get_torch()._C._cuda_getDevice()
+
+
+_torch = None
+
+
+def _get_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
 def _f32():
-    import torch
-    return torch.float32
+    return _get_torch().float32
 
 
 def _u8():
-    import torch
-    return torch.uint8
+    return _get_torch().uint8
 
 
 def _tiles(n) -> int:
@@ -647,12 +660,12 @@ def moe_layernorm_forward(x, weight, bias, eps, y, mean=None, rstd=None, dev_sta
     mean, rstd fp32 [rows] out or None."""
     ty, f32 = _type(x, "x"), _f32()
     rows, cols = x.shape
-    _mats(("x", x, (rows, cols), x.dtype), ("y", y, (rows, cols), x.dtype),
-          ("weight", weight, (cols,), f32), ("bias", bias, (cols,), f32),
-          ("mean", mean, (rows,), f32), ("rstd", rstd, (rows,), f32))
+    px, py, pw, pb, pm, pr = _mats(
+        ("x", x, (rows, cols), x.dtype), ("y", y, (rows, cols), x.dtype),
+        ("weight", weight, (cols,), f32), ("bias", bias, (cols,), f32),
+        ("mean", mean, (rows,), f32), ("rstd", rstd, (rows,), f32))
     _check("moe_layernorm_forward", lib().moe_layernorm_forward(
-        _ptr(x), ty, rows, cols, _ptr(weight), _ptr(bias), eps, _ptr(y), _ptr(mean), _ptr(rstd),
-        _ptr(dev_status), _stream(stream)))
+        px, ty, rows, cols, pw, pb, eps, py, pm, pr, _ptr(dev_status), _stream(stream)))
 
 
 def moe_layernorm_backward_workspace_size(rows, cols) -> int:
@@ -668,17 +681,17 @@ def moe_layernorm_backward(dy, x, x_scales, weight, mean, rstd, dx, dweight, dbi
     kept = xt == MOE_T_CKPT
     if kept == (x_scales is None):
         raise ValueError("x_scales goes with x kept in 8 bits")
-    _mats(("dy", dy, (rows, cols), dy.dtype),
-          ("x", x, (rows, _wide(cols) if kept else cols), x.dtype),
-          ("x_scales", x_scales, (_tiles(cols), rows), f32), ("weight", weight, (cols,), f32),
-          ("mean", mean, (rows,), f32), ("rstd", rstd, (rows,), f32),
-          ("dx", dx, (rows, cols), dy.dtype), ("dweight", dweight, (cols,), f32),
-          ("dbias", dbias, (cols,), f32))
+    pdy, px, ps, pw, pm, pr, pdx, pdw, pdb = _mats(
+        ("dy", dy, (rows, cols), dy.dtype),
+        ("x", x, (rows, _wide(cols) if kept else cols), x.dtype),
+        ("x_scales", x_scales, (_tiles(cols), rows), f32), ("weight", weight, (cols,), f32),
+        ("mean", mean, (rows,), f32), ("rstd", rstd, (rows,), f32),
+        ("dx", dx, (rows, cols), dy.dtype), ("dweight", dweight, (cols,), f32),
+        ("dbias", dbias, (cols,), f32))
     nbytes = ws.numel() * ws.element_size() if ws is not None else 0
     _check("moe_layernorm_backward", lib().moe_layernorm_backward(
-        _ptr(dy), ty, _ptr(x), xt, _ptr(x_scales), rows, cols, _ptr(weight), _ptr(mean),
-        _ptr(rstd), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, _ptr(dev_status),
-        _stream(stream)))
+        pdy, ty, px, xt, ps, rows, cols, pw, pm, pr, pdx, pdw, pdb, _ptr(ws), nbytes,
+        _ptr(dev_status), _stream(stream)))
 
 
 def moe_ckpt_row_bytes(cols) -> int:
@@ -690,20 +703,20 @@ def moe_ckpt_pack(x, q, scales, dev_status=None, stream=None):
     [ceil(cols / 128), rows]."""
     ty = _type(x, "x")
     rows, cols = x.shape
-    _mats(("x", x, (rows, cols), x.dtype), ("q", q, (rows, _wide(cols)), _u8()),
-          ("scales", scales, (_tiles(cols), rows), _f32()))
-    _check("moe_ckpt_pack", lib().moe_ckpt_pack(_ptr(x), ty, rows, cols, _ptr(q), _ptr(scales),
-                                                _ptr(dev_status), _stream(stream)))
+    px, pq, ps = _mats(("x", x, (rows, cols), x.dtype), ("q", q, (rows, _wide(cols)), _u8()),
+                       ("scales", scales, (_tiles(cols), rows), _f32()))
+    _check("moe_ckpt_pack", lib().moe_ckpt_pack(px, ty, rows, cols, pq, ps, _ptr(dev_status),
+                                                _stream(stream)))
 
 
 def moe_ckpt_unpack(q, scales, y, dev_status=None, stream=None):
     """The kept values as y [rows, cols] (its dtype)."""
     ty = _type(y, "y")
     rows, cols = y.shape
-    _mats(("y", y, (rows, cols), y.dtype), ("q", q, (rows, _wide(cols)), _u8()),
-          ("scales", scales, (_tiles(cols), rows), _f32()))
-    _check("moe_ckpt_unpack", lib().moe_ckpt_unpack(_ptr(q), _ptr(scales), rows, cols, _ptr(y), ty,
-                                                    _ptr(dev_status), _stream(stream)))
+    py, pq, ps = _mats(("y", y, (rows, cols), y.dtype), ("q", q, (rows, _wide(cols)), _u8()),
+                       ("scales", scales, (_tiles(cols), rows), _f32()))
+    _check("moe_ckpt_unpack", lib().moe_ckpt_unpack(pq, ps, rows, cols, py, ty, _ptr(dev_status),
+                                                    _stream(stream)))
 
 
 def moe_grouped_gemm_fp8_ckpt(n_groups, group_offsets, max_rows, a, a_scales, k, w, w_scales, n,
@@ -721,14 +734,14 @@ def moe_swiglu_backward_quant_ckpt(dh, ac_q, ac_scales, rows, inter, rows_total,
     """moe_swiglu_backward_quant from [a | c] kept in 8 bits; dh [>= rows,
     inter], the others rows_total rows."""
     f32, u8, n = _f32(), _u8(), 2 * inter
-    _mats(("ac_q", ac_q, (rows_total, n), u8), ("ac_scales", ac_scales, (n // 128, rows_total), f32),
-          ("dh", dh, (dh.shape[0], inter), f32), ("q", q, (rows_total, n), u8),
-          ("q_scales", q_scales, (n // 128, rows_total), f32))
+    pa, ps, ph, pq, pqs = _mats(
+        ("ac_q", ac_q, (rows_total, n), u8), ("ac_scales", ac_scales, (n // 128, rows_total), f32),
+        ("dh", dh, (dh.shape[0], inter), f32), ("q", q, (rows_total, n), u8),
+        ("q_scales", q_scales, (n // 128, rows_total), f32))
     if dh.shape[0] < rows:
         raise ValueError("dh: fewer rows than the call's")
     _check("moe_swiglu_backward_quant_ckpt", lib().moe_swiglu_backward_quant_ckpt(
-        _ptr(dh), _ptr(ac_q), _ptr(ac_scales), int(rows), int(inter), int(rows_total), _ptr(q),
-        _ptr(q_scales), _ptr(dev_status), _stream(stream)))
+        ph, pa, ps, rows, inter, rows_total, pq, pqs, _ptr(dev_status), _stream(stream)))
 
 
 def moe_wgrad_quant_h_ckpt(ac_q, ac_scales, inter, blocks, ht, ht_scales, dev_status=None,
@@ -760,12 +773,13 @@ def _kept_ac(ac, ac_scales, dtype, T, inter):
     if ac is None:
         if ac_scales is not None:
             raise ValueError("ac_scales goes with ac in 8 bits")
-        return MOE_T_CKPT, ()
+        return MOE_T_CKPT, (("ac", None, None, None), ("ac_scales", None, None, None))
     kept = ac.dtype is _u8()
     if kept == (ac_scales is None):
         raise ValueError("ac_scales goes with ac in 8 bits")
     if not kept:
-        return _type(ac, "ac"), (("ac", ac, (T, 2 * inter), dtype),)
+        return _type(ac, "ac"), (("ac", ac, (T, 2 * inter), dtype),
+                                 ("ac_scales", None, None, None))
     return MOE_T_CKPT, (("ac", ac, (T, 2 * _wide(inter)), ac.dtype),
                         ("ac_scales", ac_scales, (2 * _tiles(inter), T), _f32()))
 
@@ -778,11 +792,11 @@ def moe_ffn_forward(x, w13, w2, h, y, ac=None, ac_scales=None, dev_status=None, 
     inter = w2.shape[1]
     ty, t = _type(x, "x"), x.dtype
     at, kept = _kept_ac(ac, ac_scales, t, T, inter)
-    _mats(("x", x, (T, d), t), ("w13", w13, (2 * inter, d), t), ("w2", w2, (d, inter), t),
-          ("h", h, (T, inter), t), ("y", y, (T, d), t), *kept)
+    px, p13, p2, ph, py, pac, ps = _mats(
+        ("x", x, (T, d), t), ("w13", w13, (2 * inter, d), t), ("w2", w2, (d, inter), t),
+        ("h", h, (T, inter), t), ("y", y, (T, d), t), *kept)
     _check("moe_ffn_forward", lib().moe_ffn_forward(
-        _ptr(x), _ptr(w13), _ptr(w2), ty, T, d, inter, _ptr(h), _ptr(y), _ptr(ac), at,
-        _ptr(ac_scales), _ptr(dev_status), _stream(stream)))
+        px, p13, p2, ty, T, d, inter, ph, py, pac, at, ps, _ptr(dev_status), _stream(stream)))
 
 
 def moe_ffn_backward(dy, x, w13, w2, ac, ac_scales, dac, h, dx=None, dw13=None, dw2=None,
@@ -795,10 +809,11 @@ def moe_ffn_backward(dy, x, w13, w2, ac, ac_scales, dac, h, dx=None, dw13=None, 
     if ac is None:
         raise ValueError("moe_ffn_backward needs the kept ac")
     at, kept = _kept_ac(ac, ac_scales, t, T, inter)
-    _mats(("dy", dy, (T, d), t), ("x", x, (T, d), t), ("w13", w13, (2 * inter, d), t),
-          ("w2", w2, (d, inter), t), ("dac", dac, (T, 2 * inter), t), ("h", h, (T, inter), t),
-          ("dx", dx, (T, d), t), ("dw13", dw13, (2 * inter, d), t), ("dw2", dw2, (d, inter), t),
-          *kept)
+    pdy, px, p13, p2, pdac, ph, pdx, pd13, pd2, pac, ps = _mats(
+        ("dy", dy, (T, d), t), ("x", x, (T, d), t), ("w13", w13, (2 * inter, d), t),
+        ("w2", w2, (d, inter), t), ("dac", dac, (T, 2 * inter), t), ("h", h, (T, inter), t),
+        ("dx", dx, (T, d), t), ("dw13", dw13, (2 * inter, d), t), ("dw2", dw2, (d, inter), t),
+        *kept)
     _check("moe_ffn_backward", lib().moe_ffn_backward(
-        _ptr(dy), _ptr(x), _ptr(w13), _ptr(w2), _ptr(ac), at, _ptr(ac_scales), ty, T, d, inter,
-        _ptr(dac), _ptr(h), _ptr(dx), _ptr(dw13), _ptr(dw2), _ptr(dev_status), _stream(stream)))
+        pdy, px, p13, p2, pac, at, ps, ty, T, d, inter, pdac, ph, pdx, pd13, pd2,
+        _ptr(dev_status), _stream(stream)))

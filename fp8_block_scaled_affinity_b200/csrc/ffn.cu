@@ -520,6 +520,10 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) pair_tmem_alloc(smem_u32(&ss->tmem_base));
+    if (threadIdx.x >= 96 && threadIdx.x < 96 + 2 * a.n_problems) {
+        const Problem& p = a.p[(threadIdx.x - 96) >> 1];
+        prefetch_map(threadIdx.x & 1 ? &p.b : &p.a);
+    }
     fence_before();
     __syncthreads();
     cluster_sync();  // the peer's barriers exist before anyone signals them
@@ -551,10 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
 // out[t, r] = sum_k W[r, k] x[t, k] for 128 rows r of W a CTA: W is the M side
 // of the MMA (a row per TMEM lane), nt tokens the N side.  GATED: 64 rows of
 // W1 in lanes 0-63 and the same 64 of W3 in lanes 64-127.
-//   warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 move the accumulator
+//   warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 move the accumulator
 //   into shared memory (over the stages, all consumed by then); then every
 //   CTA of the cluster adds up its share of the tokens, ranks in order.
-constexpr int kFewThreads = 192;
+constexpr int kFewThreads = 320;
 constexpr int kFewMaxStages = 12;
 constexpr int kFewRing1 = 200 * 1024;  // stages of a CTA alone on its SM,
 constexpr int kFewRing2 = 106 * 1024;  // and of two on one
@@ -674,6 +678,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc(smem_u32(&ss->tmem_base), cols);
+    if (warp == 2 && lane == 0) {
+        prefetch_map(&a.w);
+        prefetch_map(&a.x);
+    }
     fence_before();
     __syncthreads();
     fence_after();
@@ -762,8 +770,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     fence_after();
     float* part = reinterpret_cast<float*>(smem);  // [nt][128]
     if (warp >= 2) {
-        const int q = warp & 3;
-        for (int c = 0; c < a.nt; c += 16) {
+        const int q = warp & 3;  // the quarter of the lanes it may read
+        for (int c = warp < 6 ? 0 : 16; c < a.nt; c += 32) {
             uint32_t v[16];
             if (n > 0) {
                 tmem_ld16(tmem + (uint32_t(q * 32) << 16) + c, v);
@@ -1032,10 +1040,11 @@ int backward(Maker mk, const void* dy, const void* x, const void* w13, const voi
     return rc != MOE_OK || b.n_problems == 0 ? rc : launch<kPlain, kKeptNone, T>(b, st);
 }
 
-// How a product with few tokens is laid out, and about how long it takes:
-// in SM clocks, a CTA's 16 x 16 x nt steps (2 nt clocks per 64 K elements; 128
-// is what the weights' bytes cost at least) and a fixed part for starting,
-// filling the pipeline and adding up.
+// How a product with few tokens is laid out, and about how long it takes, in
+// SM clocks fitted to 12 sizes from 16 to 1024 tokens, d and inter from 512 to
+// 7168 and 256 to 2048: for 64 K elements 3 clocks a token (the MMA's 2, and
+// the stage's bytes), 128 at least; starting, filling the pipeline, adding up
+// and writing, 7000 and 30 a token.
 struct FewPlan {
     int tiles_t, tiles_w, nt, split, ring;
     int64_t clocks;
@@ -1059,13 +1068,14 @@ FewPlan few_plan(int64_t T, int rows, int rows_per_tile, int nkb) {
            nkb >= 8 * p.split)
         p.split *= 2;
     const int64_t waves = (tiles * p.split + sms - 1) / sms;
-    p.clocks = waves * (int64_t(nkb + p.split - 1) / p.split * std::max(2 * p.nt, 128) + 6000);
+    p.clocks =
+        waves * ((nkb + p.split - 1) / p.split * int64_t(std::max(3 * p.nt, 128)) + 7000 + 30 * p.nt);
     return p;
 }
 // Whether a plan beats pair tiles of 256 x 256: only where those leave pairs
-// idle, and then by the same estimate.
+// idle, and then by the same estimate (560 clocks for 64 K elements, 9500 more).
 bool few_better(const FewPlan& p, int64_t pair_tiles, int nkb) {
-    return pair_tiles < sm_count() / 2 && p.clocks < int64_t(nkb) * 512 + 5000;
+    return pair_tiles < sm_count() / 2 && p.clocks < int64_t(nkb) * 560 + 9500;
 }
 
 template <bool GATED, int TOK, class T>

@@ -2064,11 +2064,15 @@ bool make_map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uin
 }
 
 bool device_is_sm100() {
+    static int majors[64] = {0};  // per device; 0: not asked yet
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    int major = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-        return false;
+    int major = dev >= 0 && dev < 64 ? majors[dev] : 0;
+    if (major == 0) {
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
+            return false;
+        if (dev >= 0 && dev < 64) majors[dev] = major;
+    }
     return major == 10;
 }
 

@@ -271,31 +271,38 @@ __device__ __forceinline__ uint32_t row_bytes(const Rows& m, int64_t r) {
     row_range(m, r, first, last);
     return uint32_t(last - first);
 }
-// E elements from column c of row r: from the slot the row was copied to, or
-// (the last elements of a matrix that ends inside 16 bytes) from the matrix.
-template <class T, int E>
-__device__ __forceinline__ void row_floats(const Rows& m, int64_t row_at, const char* slot, int c,
-                                           float (&f)[E]) {
-    if constexpr (E == 8) {
-        const char* p = slot + c * int(sizeof(T));
-        Raw<T, 8> v;
-        if constexpr (sizeof(T) == 4) {
-            v.a = reinterpret_cast<const float4*>(p)[0];
-            v.b = reinterpret_cast<const float4*>(p)[1];
-        } else if constexpr (sizeof(T) == 2) {
-            v.a = *reinterpret_cast<const uint4*>(p);
-        } else {
-            v.a = *reinterpret_cast<const uint2*>(p);
-        }
-        raw_floats(v, f);
-    } else {
-        const int64_t at = row_at + c * int(sizeof(T));
-        const T* p = at < m.total
-                         ? reinterpret_cast<const T*>(slot + int(row_at & 15) + c * int(sizeof(T)))
-                         : reinterpret_cast<const T*>(m.base + at);
-        f[0] = elem_float(*p);
+// A row in its slot: E elements from column c.  The last elements of a matrix
+// that ends inside 16 bytes are not in the slot (`have` columns are).
+template <class T>
+struct RowView {
+    const T* at;       // column 0 in the slot
+    const T* memory;   // and in the matrix
+    int have;
+    __device__ __forceinline__ RowView(const Rows& m, int64_t row, const char* slot, int cols) {
+        const int64_t b = row * m.pitch;
+        at = reinterpret_cast<const T*>(slot + int(b & 15));
+        memory = reinterpret_cast<const T*>(m.base + b);
+        have = int(min(int64_t(cols), (m.total - b) / int64_t(sizeof(T))));
     }
-}
+    template <int E>
+    __device__ __forceinline__ void get(int c, float (&f)[E]) const {
+        if constexpr (E == 8) {
+            const T* p = at + c;
+            Raw<T, 8> v;
+            if constexpr (sizeof(T) == 4) {
+                v.a = reinterpret_cast<const float4*>(p)[0];
+                v.b = reinterpret_cast<const float4*>(p)[1];
+            } else if constexpr (sizeof(T) == 2) {
+                v.a = *reinterpret_cast<const uint4*>(p);
+            } else {
+                v.a = *reinterpret_cast<const uint2*>(p);
+            }
+            raw_floats(v, f);
+        } else {
+            f[0] = elem_float(c < have ? at[c] : memory[c]);
+        }
+    }
+};
 
 struct Stream {
     int slot;        // bytes of a row's place
@@ -350,6 +357,7 @@ __global__ void __launch_bounds__(kStreamThreads)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         for (int i = 0; i < st.ahead; ++i) issue(blockIdx.x + int64_t(i) * G, i);
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // a row's statistics and tile scales are fetched a row (two rows) ahead;
     // there are more threads than tiles
     const int tiles = (cols + kTile - 1) / kTile;
@@ -394,6 +402,8 @@ __global__ void __launch_bounds__(kStreamThreads)
         float2 xh[P], g[P];
         float* const xf = reinterpret_cast<float*>(xh);
         float* const gf = reinterpret_cast<float*>(g);
+        const RowView<X> xr(x, row, slot, cols);
+        const RowView<T> dr(dy, row, slot + x_slot, cols);
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const int c = (t + j * tpr) * E;
@@ -401,8 +411,8 @@ __global__ void __launch_bounds__(kStreamThreads)
 #pragma unroll
             for (int e = 0; e < E; ++e) xv[e] = dv[e] = 0.0f;
             if (c < cols) {
-                row_floats<X, E>(x, row * x.pitch, slot, c, xv);
-                row_floats<T, E>(dy, row * dy.pitch, slot + x_slot, c, dv);
+                xr.get(c, xv);
+                dr.get(c, dv);
                 if (KEPT) {
                     const float sc = scale_s[par][c / kTile];
 #pragma unroll
@@ -494,6 +504,8 @@ __global__ void __launch_bounds__(1024) layernorm_sum_kernel(const float* __rest
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float a = 0.0f;
+    // (launched while the rows are still being walked)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c < 2 * cols)
 #pragma unroll 8
         for (int i = warp; i < n; i += 32) a += part[int64_t(i) * 2 * cols + c];
@@ -710,7 +722,17 @@ extern "C" MOE_API int moe_layernorm_backward(const void* dy, int type, const vo
              : type == MOE_T_BF16 ? backward_typed<bf16_t>(x_type, type, vec, a, st)
                                   : backward_typed<f16_t>(x_type, type, vec, a, st);
     if (rc != MOE_OK || !sums) return rc;
-    layernorm_sum_kernel<<<(2 * cols + 31) / 32, 1024, 0, st>>>(
-        a.part, backward_ctas(rows, cols), cols, dweight, dbias);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned((2 * cols + 31) / 32), 1, 1);
+    cfg.blockDim = dim3(1024, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, layernorm_sum_kernel, static_cast<const float*>(a.part),
+                           backward_ctas(rows, cols), cols, dweight, dbias) != cudaSuccess)
+        return MOE_ERR_CUDA;
     return check_launch();
 }

@@ -181,6 +181,11 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
                  : "memory");
 }
 
+// Fetches a tensor map before its first copy needs it.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Programmatic dependent launch: the next kernel of the stream may be
 // scheduled from here on; and the wait for everything the kernels before
 // this one have written.
