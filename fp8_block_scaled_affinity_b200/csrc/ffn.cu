@@ -12,10 +12,10 @@
 // memory (W2 and W13 in the backward pass, all operands of the weight
 // gradients) is read as it lies, as an MN-major tile: nothing is transposed
 // in memory.  The epilogues are the element-wise steps:
-//   kGated     a and c of the same 128 features lie in one tile (one CTA of
-//              the pair loads 128 rows of W1, the other 128 of W3): h, and
-//              where asked a and c kept for the backward pass, in 8 bits
-//              (1x128 tiles) or in 16;
+//   kGated     a and c of the same 128 (or 64) features lie in one tile (one
+//              CTA of the pair loads their rows of W1, the other those of W3):
+//              h, and where asked a and c kept for the backward pass, in 8
+//              bits (1x128 tiles) or in 16;
 //   kBackward  dh stays in TMEM: da, dc and h from it and the kept a, c;
 //   kPlain     the product.
 // dx, dW13 and dW2 do not depend on one another and are one launch over one
@@ -38,6 +38,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #include "elem.cuh"
@@ -75,7 +76,8 @@ struct Problem {
     CUtensorMap a, b, out;
     int m, n;                // output rows and columns
     int nkb;                 // stages of K
-    int nt;                  // tile columns (multiple of 32, at most 256)
+    int nt;                  // tile columns (multiple of 32, at most 256); kGated: of a and of c, nt / 2
+                             // features
     int tiles_m, tiles_n;
     int first;               // index of its first tile in the launch's list
     int a_mn, b_mn;          // operand's K runs along its rows in memory
@@ -125,7 +127,8 @@ struct Tile {
 
 // Tiles of a problem in groups of kGroupM row tiles, rows fastest: the tiles
 // that run side by side share few operand tiles, which stay in L2.
-__device__ __forceinline__ Tile decode(const Args& a, int t, int col_step) {
+template <int EPI>
+__device__ __forceinline__ Tile decode_for(const Args& a, int t) {
     Tile r;
     r.p = 0;
     while (r.p + 1 < a.n_problems && t >= a.p[r.p + 1].first) ++r.p;
@@ -136,13 +139,8 @@ __device__ __forceinline__ Tile decode(const Args& a, int t, int col_step) {
     const int in_g = t - g * per_group;
     const int gm = min(kGroupM, p.tiles_m - g * kGroupM);
     r.m0 = (g * kGroupM + in_g % gm) * kTileM;
-    r.n0 = (in_g / gm) * (col_step ? col_step : p.nt);
+    r.n0 = (in_g / gm) * (EPI == kGated ? p.nt / 2 : p.nt);
     return r;
-}
-
-template <int EPI>
-__device__ __forceinline__ Tile decode_for(const Args& a, int t) {
-    return decode(a, t, EPI == kGated ? 128 : 0);
 }
 
 // ------------------------------------------------ TMA producers (warps 0 and 2)
@@ -159,8 +157,8 @@ __device__ __forceinline__ void producer(const Args& a, uint8_t* smem, Shared* s
         const Tile w = decode_for<EPI>(a, t);
         const Problem& p = a.p[w.p];
         const int half = p.nt / 2;
-        // this CTA's rows of A; and of B: half the tile's columns, or 128
-        // rows of W1 (rank 0) and of W3 (rank 1)
+        // this CTA's rows of A; and of B: half the tile's columns, or the
+        // features' rows of W1 (rank 0) and of W3 (rank 1)
         const int first =
             IS_A ? w.m0 + 128 * rank : w.n0 + rank * (EPI == kGated ? a.inter : half);
         const CUtensorMap* map = IS_A ? &p.a : &p.b;
@@ -423,13 +421,13 @@ __device__ __forceinline__ void epilogue(const Args& a, Shared* ss, char* park_a
                     a.ac_scales[(wide / kTile + w.n0 / kTile) * a.rows + row] = sc;
                 }
             }
+            const int features = p.nt / 2;
 #pragma unroll 1
-            for (int ch = 0; ch < 2; ++ch) {
-                const int col = 64 * half + kChunk * ch;
+            for (int col = features / 2 * half; col < features / 2 * (half + 1); col += kChunk) {
                 const int x = w.n0 + col;
                 uint32_t va[32], vc[32];
                 tmem_ld32(tm + col, va);
-                tmem_ld32(tm + 128 + col, vc);
+                tmem_ld32(tm + features + col, vc);
                 float fa[32], fc[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
@@ -965,27 +963,47 @@ struct Maker {
     }
 };
 
-// Columns of the pair tiles of an m x n product with a K-major B: the width
-// that gives the shortest run over the device's pairs, a tile costing its
-// columns and about 64 more (filling the pipeline, its epilogue).  4096 x 7168
-// on 74 pairs: 7 rounds of 256 columns, or 7 of 224 (85 -> 80 us).  An MN-major
-// B comes in pieces of 64 columns for each half tile, so other widths load
-// what they do not use: 256 there (dy W2 in 13 tiles of 160 columns instead of
-// 8: 95 -> 110 us).
-int tile_width(int64_t m, int64_t n) {
+// The columns of a launch's pair tiles, and about how long it takes, in SM
+// clocks.  A stage of 64 K elements takes the MMA 2 clocks a column, and 100
+// more; a column of the epilogue costs `epilogue` clocks, under the next
+// tile's products but for the last tile's; starting and ending take 5500.  So
+// few tiles are cut narrow (256 tokens, d = 512, inter = 256: dy W2 14 us in one
+// tile of 256 columns, 9 us in four of 64), and many take the width whose
+// rounds over the pairs waste least (4096 x 7168 on 74 pairs: 7 rounds of 256
+// columns, or 7 of 224: 85 and 80 us).  An MN-major B comes in pieces of 64
+// columns for each half tile: 256 or 128 there, 64 with half of each piece
+// unused (13 tiles of 160 instead of 8 of 256: 110 us for 95).
+struct PairPlan {
+    int nt = 0;
+    int64_t clocks = INT64_MAX;
+};
+struct Extent {
+    int64_t m, n;
+    int nkb;
+};
+PairPlan pair_plan(const Extent* e, int count, int epilogue, std::initializer_list<int> widths) {
     const int pairs = std::max(1, sm_count() / 2);
-    int best = 256;
-    int64_t best_cost = INT64_MAX;
-    for (int nt = 256; nt >= 128; nt -= 32) {
-        const int64_t tiles = (m + kTileM - 1) / kTileM * ((n + nt - 1) / nt);
-        const int64_t cost = (tiles + pairs - 1) / pairs * (nt + 64);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = nt;
+    PairPlan best;
+    for (int nt : widths) {
+        int64_t tiles = 0, main = 0;
+        for (int i = 0; i < count; ++i) {
+            const int64_t t = (e[i].m + kTileM - 1) / kTileM * ((e[i].n + nt - 1) / nt);
+            tiles += t;
+            main += t * e[i].nkb * (2 * nt + 100);
+        }
+        if (tiles == 0) return PairPlan{256, 0};
+        main /= tiles;  // of an average tile
+        const int64_t epi = int64_t(epilogue) * nt;
+        const int64_t clocks =
+            5500 + (tiles + pairs - 1) / pairs * std::max(main, epi) + std::min(main, epi);
+        if (clocks < best.clocks) {
+            best.nt = nt;
+            best.clocks = clocks;
         }
     }
     return best;
 }
+constexpr int kPlainClocks = 8, kGatedClocks = 16, kBackwardClocks = 66;
 
 // out [m, n] = A B^T over k: A is [m, k] in memory, or [k, m] (a_mn); B is
 // [n, k], or [k, n] (b_mn).
@@ -1025,14 +1043,21 @@ int backward(Maker mk, const void* dy, const void* x, const void* w13, const voi
     Args a = make_args(rows, I, dev_status);
     a.ac = ac;
     a.ac_scales = const_cast<float*>(ac_scales);
-    product(a, mk, dy, false, w2, true, h, rows, I, d, 256);
+    const int kd = (d + kTileK - 1) / kTileK, kt = int((rows + kTileK - 1) / kTileK);
+    const Extent ea = {rows, I, kd};
+    product(a, mk, dy, false, w2, true, h, rows, I, d,
+            pair_plan(&ea, 1, kBackwardClocks, {256, 128, 64}).nt);
     mk.output(&a.p[0].out, dac, rows, I, 2 * int64_t(I));
     mk.output(&a.o1, static_cast<uint16_t*>(dac) + I, rows, I, 2 * int64_t(I));
     mk.output(&a.o2, h, rows, I, I);
     Args b = make_args(rows, I, dev_status);
-    if (dx) product(b, mk, dac, false, w13, true, dx, rows, d, 2 * int64_t(I), 256);
-    if (dw13) product(b, mk, dac, true, x, true, dw13, 2 * int64_t(I), d, rows, 256);
-    if (dw2) product(b, mk, dy, true, h, true, dw2, d, I, rows, 256);
+    const Extent eb[3] = {{dx ? rows : 0, d, (2 * I + kTileK - 1) / kTileK},
+                          {dw13 ? 2 * int64_t(I) : 0, d, kt},
+                          {dw2 ? d : 0, I, kt}};
+    const int nt = pair_plan(eb, 3, kPlainClocks, {256, 128, 64}).nt;
+    if (dx) product(b, mk, dac, false, w13, true, dx, rows, d, 2 * int64_t(I), nt);
+    if (dw13) product(b, mk, dac, true, x, true, dw13, 2 * int64_t(I), d, rows, nt);
+    if (dw2) product(b, mk, dy, true, h, true, dw2, d, I, rows, nt);
     b.wait_first = 1;
     if (!mk.ok) return MOE_ERR_CUDA;
     const int rc = kept == kKept8 ? launch<kBackward, kKept8, T>(a, st)
@@ -1072,10 +1097,11 @@ FewPlan few_plan(int64_t T, int rows, int rows_per_tile, int nkb) {
         waves * ((nkb + p.split - 1) / p.split * int64_t(std::max(3 * p.nt, 128)) + 7000 + 30 * p.nt);
     return p;
 }
-// Whether a plan beats pair tiles of 256 x 256: only where those leave pairs
-// idle, and then by the same estimate (560 clocks for 64 K elements, 9500 more).
-bool few_better(const FewPlan& p, int64_t pair_tiles, int nkb) {
-    return pair_tiles < sm_count() / 2 && p.clocks < int64_t(nkb) * 560 + 9500;
+// Whether a plan beats pairs: only where tiles of 256 x 256 leave pairs idle,
+// and then by the two estimates.
+bool few_better(const FewPlan& p, int64_t m, int64_t n, const PairPlan& pair) {
+    return (m + kTileM - 1) / kTileM * ((n + 255) / 256) < sm_count() / 2 &&
+           p.clocks < pair.clocks;
 }
 
 template <bool GATED, int TOK, class T>
@@ -1155,13 +1181,16 @@ int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t ro
             void* h, void* y, void* ac, int kept, float* ac_scales, int* dev_status,
             cudaStream_t st) {
     const int kd = (d + kTileK - 1) / kTileK, ki = (I + kTileK - 1) / kTileK;
-    const int64_t tiles_m = (rows + kTileM - 1) / kTileM;
-    const FewPlan fa = few_plan(rows, I, 64, kd), fb = few_plan(rows, d, 128, ki);
     // few tokens: whichever way takes fewer clocks.  (One token, d = 7168,
     // inter = 2048: 70 us in pairs of CTAs.)  What is kept comes from the pairs'
-    // epilogue, which sees 128 features of a and c together.
-    const bool few_a = kept == kKeptNone && few_better(fa, tiles_m * ((I + 127) / 128), kd);
-    const bool few_b = few_better(fb, tiles_m * ((d + 255) / 256), ki);
+    // epilogue, and in 8 bits from tiles that see 128 features together.
+    const Extent ea = {rows, 2 * int64_t(I), kd}, eb = {rows, d, ki};
+    const PairPlan pa = kept == kKept8 ? pair_plan(&ea, 1, kGatedClocks, {256})
+                                       : pair_plan(&ea, 1, kGatedClocks, {256, 128});
+    const PairPlan pb = pair_plan(&eb, 1, kPlainClocks, {256, 224, 192, 160, 128, 96, 64});
+    const FewPlan fa = few_plan(rows, I, 64, kd), fb = few_plan(rows, d, 128, ki);
+    const bool few_a = kept == kKeptNone && few_better(fa, rows, 2 * int64_t(I), pa);
+    const bool few_b = few_better(fb, rows, d, pb);
     int rc;
     // One token, or a few with few weights (a token's multiplications cost as
     // much time as its weights' bytes: 2 and 4 tokens of 88 MB of weights take
@@ -1177,11 +1206,11 @@ int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t ro
         if (few_b) return launch_few<false, T>(mk, fb, w2, h, y, rows, d, I, dev_status, true, st);
     }
     Args a = make_args(rows, I, dev_status);
-    product(a, mk, x, false, w13, false, h, rows, 2 * int64_t(I), d, 256);
-    // the gated tile: 128 features of W1 and of W3
+    product(a, mk, x, false, w13, false, h, rows, 2 * int64_t(I), d, pa.nt);
+    // the gated tile: nt / 2 features of W1 and of W3
     Problem& p = a.p[0];
     p.n = I;
-    p.tiles_n = (I + 127) / 128;
+    p.tiles_n = (I + pa.nt / 2 - 1) / (pa.nt / 2);
     a.tiles = p.tiles_m * p.tiles_n;
     mk.output(&p.out, h, rows, I, I);
     a.ac = ac;
@@ -1191,7 +1220,7 @@ int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t ro
         mk.output(&a.o2, static_cast<uint16_t*>(ac) + I, rows, I, 2 * int64_t(I));
     }
     Args b = make_args(rows, I, dev_status);
-    product(b, mk, h, false, w2, false, y, rows, d, I, tile_width(rows, d));
+    product(b, mk, h, false, w2, false, y, rows, d, I, pb.nt);
     b.wait_first = 1;
     if (!mk.ok) return MOE_ERR_CUDA;
     if (!few_a) {
