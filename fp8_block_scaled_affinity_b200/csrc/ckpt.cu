@@ -190,10 +190,12 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_ckpt_kernel(
             da[r][i] = mul2(mul2(hs, c), t);
             dc[r][i] = mul2(hs, a);
         }
-        const float ma = fmaxf(fmaxf(fabsf(da[r][0].x), fabsf(da[r][0].y)),
-                               fmaxf(fabsf(da[r][1].x), fabsf(da[r][1].y)));
-        const float mc = fmaxf(fmaxf(fabsf(dc[r][0].x), fabsf(dc[r][0].y)),
-                               fmaxf(fabsf(dc[r][1].x), fabsf(dc[r][1].y)));
+        float ma = 0.0f, mc = 0.0f;  // (a NaN is no maximum)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            ma = fmaxf(fmaxf(ma, fabsf(da[r][i].x)), fabsf(da[r][i].y));
+            mc = fmaxf(fmaxf(mc, fabsf(dc[r][i].x)), fabsf(dc[r][i].y));
+        }
         // the warp's maxima: as integers, whose order is that of |v|
         const uint32_t wa = __reduce_max_sync(0xffffffffu, __float_as_uint(ma));
         const uint32_t wc = __reduce_max_sync(0xffffffffu, __float_as_uint(mc));

@@ -196,7 +196,7 @@ __device__ __forceinline__ void producer(const Args& a, uint8_t* smem, Shared* s
         for (int i = 0; i < kStages; ++i)
             if ((issued >> i) & 1u)
                 mbar_quiesce(smem_u32(&ss->full[i]), (issued_parity >> i) & 1u, nullptr,
-                             ss->ps.wait_limit);
+                             quiesce_ns(ss->ps.wait_limit));
     __syncwarp();
 }
 
@@ -247,7 +247,7 @@ __device__ __forceinline__ void issuer(const Args& a, uint8_t* smem, Shared* ss,
     if (lead) {
         // every MMA has completed once this fires (after an abort too)
         pair_commit(smem_u32(&ss->drain));
-        mbar_quiesce(smem_u32(&ss->drain), 0, nullptr, ss->ps.wait_limit);
+        mbar_quiesce(smem_u32(&ss->drain), 0, nullptr, quiesce_ns(ss->ps.wait_limit));
     }
     __syncwarp();
 }
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         if (!ok && lead)  // loads in flight land before the CTA leaves
             for (int j = max(0, i - a.stages); j < i; ++j)
                 mbar_quiesce(smem_u32(&ss->full[j % a.stages]), (j / a.stages) & 1u, nullptr,
-                             a.wait_limit_ns);
+                             quiesce_ns(a.wait_limit_ns));
     } else if (warp == 1) {
         const bool lead = elect_one();
         const uint32_t idesc = idesc_f16(std::is_same<T, bf16_t>::value, 0, 0, 128, a.nt);
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         }
         if (lead) {
             commit(smem_u32(&ss->done));
-            mbar_quiesce(smem_u32(&ss->done), 0, nullptr, a.wait_limit_ns);
+            mbar_quiesce(smem_u32(&ss->done), 0, nullptr, quiesce_ns(a.wait_limit_ns));
         }
     }
     __syncwarp();

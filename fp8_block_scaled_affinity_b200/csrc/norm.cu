@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kStreamThreads)
         for (int k = 0; k < st.ahead; ++k, row += G, turn.next(st.ahead))
             if (row < rows)
                 tc::mbar_quiesce(tc::smem_u32(&ss.full[turn.slot]), turn.phase, nullptr,
-                                 st.wait_limit_ns);
+                                 tc::quiesce_ns(st.wait_limit_ns));
     if (!part) return;
     float* p = part + int64_t(blockIdx.x) * 2 * cols;
 #pragma unroll
@@ -682,7 +682,8 @@ extern "C" MOE_API int moe_layernorm_forward(const void* x, int type, int64_t ro
     if (rows == 0) return MOE_OK;
     if (!x || !y) return MOE_ERR_NULL;
     const size_t es = type_size(type);
-    if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, 4) || !aligned(bias, 4))
+    if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, 4) || !aligned(bias, 4) ||
+        !aligned(mean, 4) || !aligned(rstd, 4))
         return MOE_ERR_ALIGN;
     if (!device_is_sm100()) return MOE_ERR_DEVICE;
     const bool vec = cols % 4 == 0 && aligned16(x) && aligned16(y) && aligned16(weight) &&
@@ -722,7 +723,9 @@ extern "C" MOE_API int moe_layernorm_backward(const void* dy, int type, const vo
     if (!dy || !x || !mean || !rstd || !dx) return MOE_ERR_NULL;
     if (x_type == MOE_T_CKPT && !x_scales) return MOE_ERR_NULL;
     const size_t es = type_size(type);
-    if (!aligned(dy, es) || !aligned(dx, es) || !aligned(weight, 4) || !aligned(x, type_size(x_type)))
+    if (!aligned(dy, es) || !aligned(dx, es) || !aligned(weight, 4) ||
+        !aligned(x, type_size(x_type)) || !aligned(x_scales, 4) || !aligned(mean, 4) ||
+        !aligned(rstd, 4) || !aligned(dweight, 4) || !aligned(dbias, 4))
         return MOE_ERR_ALIGN;
     if (x_type == MOE_T_CKPT && !aligned16(x)) return MOE_ERR_ALIGN;
     const bool sums = dweight || dbias;

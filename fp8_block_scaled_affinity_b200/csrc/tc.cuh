@@ -75,6 +75,11 @@ __device__ __forceinline__ bool mbar_quiesce(uint32_t bar, uint32_t parity, int*
     }
 }
 
+// Limit of such a wait where the launch's own may be shorter than a load takes.
+__device__ __forceinline__ uint64_t quiesce_ns(uint64_t limit_ns) {
+    return limit_ns > 1000000ull ? limit_ns : 1000000ull;
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int x, int y) {
     asm volatile(

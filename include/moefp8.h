@@ -797,7 +797,7 @@ MOE_API int moe_layernorm_backward(const void* dy, int type, const void* x, int 
  * moe_ckpt_row_bytes: cols rounded up to a multiple of 128 (-1 when cols is
  *   negative or above 2^31 - 1).
  * moe_ckpt_pack: x [rows, cols] of `type` (MOE_T_F32, _BF16, _F16) -> q,
- *   scales.  Any cols; x aligned to its element, fast for cols % 8 == 0 and
+ *   scales.  Any cols up to 33553920; x aligned to its element, fast for cols % 8 == 0 and
  *   16-byte aligned x.
  * moe_ckpt_unpack: y = type(fp32(code scale)).
  *
