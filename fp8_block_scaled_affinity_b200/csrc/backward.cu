@@ -183,70 +183,11 @@ __global__ void __launch_bounds__(256) swiglu_backward_quant_kernel(
 }
 
 // ------------------------------------------- 6. gate gradients (FP64)
-// A warp per token: dg_k = <dy, o_k> summed in FP64.  A lane takes four
-// consecutive values per step (one 8-byte load of dy, one 16-byte load of
-// each of the KM rows, all in flight together) and keeps KM FP64 partial
-// sums; one shuffle tree per slot at the end.  Then the chosen scores'
-// gradients in FP64.
-// OT: float, or e4m3_t for outputs kept in 8 bits: the warp's 128 columns of
-// a step are one tile, whose scale multiplies the lane's four exact products'
-// sum once.
-template <class OT, int KM>
-__global__ void __launch_bounds__(256) gate_backward_kernel(
-    const uint16_t* __restrict__ dy, const OT* __restrict__ o,
-    const float* __restrict__ o_scales, int64_t o_rows, int T, int d, int K,
-    const int32_t* __restrict__ row_of_pair, const float* __restrict__ score,
-    float* __restrict__ dgate, float* __restrict__ du) {
-    constexpr bool KEPT = sizeof(OT) == 1;
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-    if (t >= T) return;
-    const OT* rows[KM];
-    int row_at[KM];  // KEPT: the row's index in o_scales
-    double acc[KM];
-#pragma unroll
-    for (int k = 0; k < KM; ++k) {
-        const int row = k < K ? row_of_pair[int64_t(t) * K + k] : -1;
-        rows[k] = row >= 0 ? o + int64_t(row) * d : nullptr;
-        row_at[k] = row;
-        acc[k] = 0.0;
-    }
-    const uint2* dyr = reinterpret_cast<const uint2*>(dy + int64_t(t) * d);
-    for (int c = lane; c < d / 4; c += 32) {
-        const uint2 w = __ldg(dyr + c);
-        const double y0 = bf16_lo(w.x), y1 = bf16_hi(w.x), y2 = bf16_lo(w.y), y3 = bf16_hi(w.y);
-        if constexpr (KEPT) {
-            uint32_t q[KM];
-            float sc[KM];
-#pragma unroll
-            for (int k = 0; k < KM; ++k) {
-                q[k] = 0u;
-                sc[k] = 0.0f;
-                if (rows[k]) {
-                    q[k] = __ldg(reinterpret_cast<const uint32_t*>(rows[k]) + c);
-                    sc[k] = __ldg(o_scales + int64_t(c / 32) * o_rows + row_at[k]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < KM; ++k) {
-                // a bf16 value times a code is exact in fp32, their sums FP64
-                const float2 lo = e4m3x2_to_float2(uint16_t(q[k] & 0xFFFFu));
-                const float2 hi = e4m3x2_to_float2(uint16_t(q[k] >> 16));
-                acc[k] += double(sc[k]) * (y0 * double(lo.x) + y1 * double(lo.y) +
-                                           y2 * double(hi.x) + y3 * double(hi.y));
-            }
-        } else {
-            float4 v[KM];
-#pragma unroll
-            for (int k = 0; k < KM; ++k)
-                v[k] = rows[k] ? __ldg(reinterpret_cast<const float4*>(rows[k]) + c)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < KM; ++k)
-                acc[k] += y0 * double(v[k].x) + y1 * double(v[k].y) + y2 * double(v[k].z) +
-                          y3 * double(v[k].w);
-        }
-    }
+// The rest of a token's warp from each slot's lane sums: dg_k, and the chosen
+// scores' gradients in FP64.
+template <int KM>
+__device__ __forceinline__ void gate_finish(const double (&acc)[KM], int64_t t, int K, int lane,
+                                            const float* score, float* dgate, float* du) {
     double my_dg = 0.0;
 #pragma unroll
     for (int k = 0; k < KM; ++k) {
@@ -255,7 +196,7 @@ __global__ void __launch_bounds__(256) gate_backward_kernel(
         for (int s2 = 16; s2 >= 1; s2 >>= 1) a += __shfl_xor_sync(0xffffffffu, a, s2);
         if (lane == k) my_dg = a;
     }
-    const double s = lane < K ? double(score[int64_t(t) * K + lane]) : 0.0;
+    const double s = lane < K ? double(score[t * K + lane]) : 0.0;
     double S = s;
 #pragma unroll
     for (int o2 = 16; o2 >= 1; o2 >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o2);
@@ -264,9 +205,113 @@ __global__ void __launch_bounds__(256) gate_backward_kernel(
     for (int o2 = 16; o2 >= 1; o2 >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o2);
     if (lane < K) {
         const double ds = (my_dg - term) / S;
-        dgate[int64_t(t) * K + lane] = float(my_dg);
-        du[int64_t(t) * K + lane] = float(ds * s * (1.0 - s));
+        dgate[t * K + lane] = float(my_dg);
+        du[t * K + lane] = float(ds * s * (1.0 - s));
     }
+}
+
+// A warp per token: dg_k = <dy, o_k> summed in FP64.  A lane takes four
+// consecutive values per step (one 8-byte load of dy, one 16-byte load of
+// each of the KM rows, all in flight together) and keeps KM FP64 partial
+// sums; one shuffle tree per slot at the end.  Then the chosen scores'
+// gradients in FP64.
+template <int KM>
+__global__ void __launch_bounds__(256) gate_backward_kernel(
+    const uint16_t* __restrict__ dy, const float* __restrict__ o, int T, int d, int K,
+    const int32_t* __restrict__ row_of_pair, const float* __restrict__ score,
+    float* __restrict__ dgate, float* __restrict__ du) {
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+    if (t >= T) return;
+    const float4* rows[KM];
+    double acc[KM];
+#pragma unroll
+    for (int k = 0; k < KM; ++k) {
+        const int row = k < K ? row_of_pair[int64_t(t) * K + k] : -1;
+        rows[k] = row >= 0 ? reinterpret_cast<const float4*>(o + int64_t(row) * d) : nullptr;
+        acc[k] = 0.0;
+    }
+    const uint2* dyr = reinterpret_cast<const uint2*>(dy + int64_t(t) * d);
+    for (int c = lane; c < d / 4; c += 32) {
+        const uint2 w = __ldg(dyr + c);
+        const double y0 = bf16_lo(w.x), y1 = bf16_hi(w.x), y2 = bf16_lo(w.y), y3 = bf16_hi(w.y);
+        float4 v[KM];
+#pragma unroll
+        for (int k = 0; k < KM; ++k)
+            v[k] = rows[k] ? __ldg(rows[k] + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < KM; ++k)
+            acc[k] += y0 * double(v[k].x) + y1 * double(v[k].y) + y2 * double(v[k].z) +
+                      y3 * double(v[k].w);
+    }
+    gate_finish<KM>(acc, t, K, lane, score, dgate, du);
+}
+
+// The same from outputs kept in 8 bits.  A lane takes 16 consecutive values of
+// a row (one 16-byte load of each of up to eight rows in flight), which lie in
+// one tile: the products are exact in fp32, their 16 are summed there and
+// scaled once (relative error under 10 x 2^-24 of the terms' absolute values),
+// and these sums add up in FP64.  4096 tokens with 8 experts of d = 7168
+// (0.3 GB, 0.05 ms at the copy rate) took 0.56 ms in FP64 throughout, where
+// every value is converted, and take 0.08 ms so.
+template <int KM>
+__global__ void __launch_bounds__(256) gate_backward_kept_kernel(
+    const uint16_t* __restrict__ dy, const uint8_t* __restrict__ o,
+    const float* __restrict__ o_scales, int64_t o_rows, int T, int d, int K,
+    const int32_t* __restrict__ row_of_pair, const float* __restrict__ score,
+    float* __restrict__ dgate, float* __restrict__ du) {
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+    if (t >= T) return;
+    int rows[KM];
+    double acc[KM];
+#pragma unroll
+    for (int k = 0; k < KM; ++k) {
+        rows[k] = k < K ? row_of_pair[int64_t(t) * K + k] : -1;
+        acc[k] = 0.0;
+    }
+    const uint16_t* dyr = dy + int64_t(t) * d;
+    constexpr int B = KM < 8 ? KM : 8;  // rows in flight
+    for (int c = 16 * lane; c < d; c += 512) {
+        float y[16];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(dyr + c) + h);
+            y[4 * h] = bf16_lo(w.x);
+            y[4 * h + 1] = bf16_hi(w.x);
+            y[4 * h + 2] = bf16_lo(w.y);
+            y[4 * h + 3] = bf16_hi(w.y);
+        }
+#pragma unroll
+        for (int k0 = 0; k0 < KM; k0 += B) {
+            uint4 q[B];
+            float sc[B];
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                q[k] = make_uint4(0u, 0u, 0u, 0u);
+                sc[k] = 0.0f;
+                if (rows[k0 + k] >= 0) {
+                    q[k] = __ldcs(
+                        reinterpret_cast<const uint4*>(o + int64_t(rows[k0 + k]) * d + c));
+                    sc[k] = __ldg(o_scales + int64_t(c / kTile) * o_rows + rows[k0 + k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+                float2 a = both(0.0f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a = fma2(e4m3x2_to_float2(uint16_t(w[i] & 0xFFFFu)),
+                             make_float2(y[4 * i], y[4 * i + 1]), a);
+                    a = fma2(e4m3x2_to_float2(uint16_t(w[i] >> 16)),
+                             make_float2(y[4 * i + 2], y[4 * i + 3]), a);
+                }
+                acc[k0 + k] += double((a.x + a.y) * sc[k]);
+            }
+        }
+    }
+    gate_finish<KM>(acc, t, K, lane, score, dgate, du);
 }
 
 // ------------------------------------------- 7. router gradients
@@ -712,27 +757,6 @@ RouterBwdWs router_bwd_ws(const MoeShape& s) {
     return w;
 }
 
-template <class OT>
-int launch_gate_backward(const MoeShape* s, const uint16_t* dy, const OT* o, const float* o_scales,
-                         const int32_t* row_of_pair, const float* score, float* dgate, float* du,
-                         cudaStream_t st) {
-    const int T = s->T, K = s->topk, grid = (T + 7) / 8;
-    const int64_t R = int64_t(T) * K + T;
-    if (K <= 4)
-        gate_backward_kernel<OT, 4><<<grid, 256, 0, st>>>(dy, o, o_scales, R, T, s->d, K,
-                                                          row_of_pair, score, dgate, du);
-    else if (K <= 8)
-        gate_backward_kernel<OT, 8><<<grid, 256, 0, st>>>(dy, o, o_scales, R, T, s->d, K,
-                                                          row_of_pair, score, dgate, du);
-    else if (K <= 16)
-        gate_backward_kernel<OT, 16><<<grid, 256, 0, st>>>(dy, o, o_scales, R, T, s->d, K,
-                                                           row_of_pair, score, dgate, du);
-    else
-        gate_backward_kernel<OT, 32><<<grid, 256, 0, st>>>(dy, o, o_scales, R, T, s->d, K,
-                                                           row_of_pair, score, dgate, du);
-    return check_launch();
-}
-
 int pieces_per(int n, int& PC) {
     const int nkb = n / 128;
     PC = (nkb % 14 == 0 && nkb % 16 != 0) ? 7 : 8;
@@ -820,9 +844,22 @@ extern "C" MOE_API int moe_gate_backward(const MoeShape* shape, const uint16_t* 
     const int T = shape->T;
     if (T == 0) return MOE_OK;
     if (!dy || !expert_out || !row_of_pair || !topk_score || !dgate || !du) return MOE_ERR_NULL;
+    const int K = shape->topk, grid = (T + 7) / 8;
+    cudaStream_t st = as_stream(stream);
     if (!aligned16(expert_out) || (reinterpret_cast<uintptr_t>(dy) & 7)) return MOE_ERR_ALIGN;
-    return launch_gate_backward<float>(shape, dy, expert_out, nullptr, row_of_pair, topk_score,
-                                       dgate, du, as_stream(stream));
+    if (K <= 4)
+        gate_backward_kernel<4><<<grid, 256, 0, st>>>(dy, expert_out, T, shape->d, K, row_of_pair,
+                                                      topk_score, dgate, du);
+    else if (K <= 8)
+        gate_backward_kernel<8><<<grid, 256, 0, st>>>(dy, expert_out, T, shape->d, K, row_of_pair,
+                                                      topk_score, dgate, du);
+    else if (K <= 16)
+        gate_backward_kernel<16><<<grid, 256, 0, st>>>(dy, expert_out, T, shape->d, K,
+                                                       row_of_pair, topk_score, dgate, du);
+    else
+        gate_backward_kernel<32><<<grid, 256, 0, st>>>(dy, expert_out, T, shape->d, K,
+                                                       row_of_pair, topk_score, dgate, du);
+    return check_launch();
 }
 
 extern "C" MOE_API int moe_gate_backward_ckpt(const MoeShape* shape, const uint16_t* dy,
@@ -837,8 +874,17 @@ extern "C" MOE_API int moe_gate_backward_ckpt(const MoeShape* shape, const uint1
     if (!dy || !o_q || !o_scales || !row_of_pair || !topk_score || !dgate || !du)
         return MOE_ERR_NULL;
     if (!aligned16(o_q) || (reinterpret_cast<uintptr_t>(dy) & 7)) return MOE_ERR_ALIGN;
-    return launch_gate_backward<e4m3_t>(shape, dy, reinterpret_cast<const e4m3_t*>(o_q), o_scales,
-                                        row_of_pair, topk_score, dgate, du, as_stream(stream));
+    const int T = shape->T, K = shape->topk, grid = (T + 7) / 8;
+    const int64_t R = int64_t(T) * K + T;
+    auto go = [&](auto kernel) {
+        kernel<<<grid, 256, 0, as_stream(stream)>>>(dy, o_q, o_scales, R, T, shape->d, K,
+                                                    row_of_pair, topk_score, dgate, du);
+        return check_launch();
+    };
+    if (K <= 4) return go(gate_backward_kept_kernel<4>);
+    if (K <= 8) return go(gate_backward_kept_kernel<8>);
+    if (K <= 16) return go(gate_backward_kept_kernel<16>);
+    return go(gate_backward_kept_kernel<32>);
 }
 
 extern "C" MOE_API int moe_router_backward(const MoeShape* shape, const uint16_t* x,

@@ -813,7 +813,8 @@ MOE_API int moe_layernorm_backward(const void* dy, int type, const void* x, int 
  * moe_wgrad_quant_h_ckpt, moe_wgrad_quant_dac_ckpt: moe_wgrad_quant_h and
  *   _dac with [a | c] kept so; rows_total is the scales' row length.
  * moe_gate_backward_ckpt: moe_gate_backward with the expert outputs kept as
- *   o_q (uint8 [R, d]) and o_scales (fp32 [d / 128, R]), R = T K + T.
+ *   o_q (uint8 [R, d]) and o_scales (fp32 [d / 128, R]), R = T K + T; 16
+ *   products at a time are summed in fp32, those sums in FP64.
  * Errors: MOE_ERR_ARG, MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_ALIGN,
  * MOE_ERR_DEVICE, MOE_ERR_CUDA. */
 MOE_API int64_t moe_ckpt_row_bytes(int64_t cols);
