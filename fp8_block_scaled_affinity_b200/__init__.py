@@ -9,6 +9,8 @@ raises.
 """
 from __future__ import annotations
 
+import functools
+import inspect
 from typing import Optional
 
 from ._lib import (MOE_DEV_TIMEOUT, MOE_EPI_BF16, MOE_EPI_F32, MOE_EPI_SWIGLU_QUANT,  # noqa: F401
@@ -42,9 +44,33 @@ from ._lib import (MOE_DEV_TIMEOUT, MOE_EPI_BF16, MOE_EPI_F32, MOE_EPI_SWIGLU_QU
 __all__ = ["MoeLayer", "GatedFfn", "LayerNorm", "MoeShape", "MoeError", "lib", "make_shape", "moe_version"]
 
 
+def _on_stream(method):
+    """A method whose `stream` is made the current stream while it runs, so
+    that its buffers come from that stream's memory: one that is let go of
+    when the call returns is not handed out again before the stream is past it."""
+    at = list(inspect.signature(method).parameters).index("stream")
+
+    @functools.wraps(method)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return method(*args, **kw)
+        import torch
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):
+            return method(*args, **kw)
+    return call
+
+
 def _check_keep(keep):
     if keep not in ("full", "fp8"):
         raise ValueError("keep must be 'full' or 'fp8'")
+
+
+def _check_not_over(y, x):
+    if y.data_ptr() == x.data_ptr() and y.numel():
+        raise ValueError("y may not be x, which is kept for backward()")
 
 
 def _pack(x, stream):
@@ -62,7 +88,7 @@ class LayerNorm:
     GPU, or None) and what its backward pass needs of the last forward_train.
 
     forward_train(x, keep): keep="full" keeps x itself (it must stay unchanged
-    until backward() has run), "fp8" an 8-bit copy of it.  backward(dy) leaves
+    until backward() has run, so y may not be x), "fp8" an 8-bit copy of it.  backward(dy) leaves
     the parameters' gradients in dweight and dbias (fp32)."""
 
     def __init__(self, weight=None, bias=None, eps: float = 1e-5):
@@ -70,6 +96,7 @@ class LayerNorm:
         self.dweight = self.dbias = None
         self._kept = None
 
+    @_on_stream
     def forward(self, x, y=None, stream=None):
         import torch
         if y is None:
@@ -77,18 +104,23 @@ class LayerNorm:
         moe_layernorm_forward(x, self.weight, self.bias, self.eps, y, stream=stream)
         return y
 
+    @_on_stream
     def forward_train(self, x, y=None, keep: str = "full", stream=None):
         """forward(), the same bits, keeping what backward() needs."""
         import torch
         _check_keep(keep)
         if y is None:
             y = torch.empty_like(x)
+        elif keep == "full":
+            _check_not_over(y, x)
         stats = [torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
                  for _ in range(2)]
+        kept = _pack(x, stream) if keep == "fp8" else (x, None)  # first: y may be x
         moe_layernorm_forward(x, self.weight, self.bias, self.eps, y, *stats, stream=stream)
-        self._kept = (_pack(x, stream) if keep == "fp8" else (x, None)) + tuple(stats)
+        self._kept = kept + tuple(stats)
         return y
 
+    @_on_stream
     def backward(self, dy, stream=None):
         """dx (dy's type) of the last forward_train(); dy of x's type or fp32."""
         import torch
@@ -125,6 +157,7 @@ class GatedFfn:
         import torch
         return torch.empty((x.shape[0], cols), dtype=x.dtype, device=x.device)
 
+    @_on_stream
     def forward(self, x, y=None, stream=None):
         """y for x [T, d] on the GPU."""
         import torch
@@ -135,6 +168,7 @@ class GatedFfn:
                         dev_status=self.dev_status, stream=stream)
         return y
 
+    @_on_stream
     def forward_train(self, x, y=None, keep: str = "fp8", stream=None):
         """forward(), keeping what backward() needs: the block's input (x, or
         the norm's output) as it is, and gate and up, and the norm's input, in
@@ -143,6 +177,8 @@ class GatedFfn:
         import torch
         _check_keep(keep)
         T, inter = x.shape[0], self.w2.shape[1]
+        if y is not None and (self.norm is None or keep == "full"):
+            _check_not_over(y, x)
         n = x if self.norm is None else self.norm.forward_train(x, keep=keep, stream=stream)
         if y is None:
             y = torch.empty_like(x)
@@ -157,6 +193,7 @@ class GatedFfn:
         self._kept = (n, ac, scales)
         return y
 
+    @_on_stream
     def backward(self, dy, wgrad: bool = True, stream=None):
         """Gradients of the last forward_train(): dx, or with wgrad
         (dx, dw13, dw2), all of the block's dtype; a norm's parameters'
@@ -254,6 +291,7 @@ class MoeLayer:
             self._weights = mk(self.w13, self.w13_scales, self.w2, self.w2_scales, self.router_w)
         return self._weights
 
+    @_on_stream
     def forward(self, x, y=None, update_bias: bool = False, logit_offset=None, stream=None):
         """y = MoE(x) for bf16 x [T, d] on the GPU; returns y (bf16 [T, d])."""
         import torch
@@ -308,6 +346,7 @@ class MoeLayer:
             }
         return self._train
 
+    @_on_stream
     def forward_train(self, x, y=None, update_bias: bool = False, logit_offset=None,
                       stream=None, keep: Optional[str] = None):
         """The forward pass (fp32-scale recipe) through the stage entry points,
@@ -380,6 +419,7 @@ class MoeLayer:
             self._transposed = (w2t, w2t_s, w13t, w13t_s)
         return self._transposed
 
+    @_on_stream
     def backward(self, dy, stream=None, marks=None, wgrad: bool = False):
         """Gradients of the last forward_train() for the upstream gradient dy
         (bf16 [T, d]): returns (dx fp32 [T, d], d_router_w fp32 [N_r, d]), and

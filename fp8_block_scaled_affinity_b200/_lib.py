@@ -609,7 +609,8 @@ def _mats(first, *specs):
     Returns the tensors' addresses (None for None)."""
     name, t, shape, dtype = first
     dev = t.get_device()
-    if dev < 0 or dev != _current_device() or t.shape != shape or not t.is_contiguous():
+    if (dev < 0 or dev != _current_device() or t.dtype is not dtype or t.shape != shape
+            or not t.is_contiguous()):
         _mat(name, t, shape, dtype)
     at = [t.data_ptr()]
     for name, t, shape, dtype in specs:

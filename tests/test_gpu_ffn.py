@@ -316,3 +316,26 @@ def test_side_streams_at_once_and_captured(T):
     torch.cuda.synchronize()
     for a, b in zip(got, two[0][3]):
         assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """Tokens whose elements lie beyond 2^31 give what the same tokens give in
+    a call that takes the same tiles."""
+    import fp8_block_scaled_affinity_b200 as moe
+    need_gpu()
+    d, I = 4096, 64
+    T = 2 ** 31 // d + 4096
+    w13, w2 = rand(2 * I, d, seed=2, scale=d ** -0.5, dt=torch.bfloat16), rand(d, I, seed=3, dt=torch.bfloat16)
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device=DEV)
+    x[-4096:] = rand(4096, d, seed=1, dt=torch.bfloat16)
+
+    def step(x):
+        n = x.shape[0]
+        e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+        h, y, dac, h2, dx = e(n, I), e(n, d), e(n, 2 * I), e(n, I), e(n, d)
+        ac, s = torch.empty(n, 256, dtype=torch.uint8, device=DEV), torch.empty(2, n, device=DEV)
+        moe.moe_ffn_forward(x, w13, w2, h, y, ac, s)
+        moe.moe_ffn_backward(x, x, w13, w2, ac, s, dac, h2, dx)
+        return [v[-4096:] for v in (h, y, ac, s.t(), dac, h2, dx)]
+    for a, b in zip(step(x), step(x[-4096:].clone())):
+        assert torch.equal(a, b)

@@ -265,3 +265,61 @@ def test_refusals():
     with pytest.raises(ValueError, match="norm"):
         moe.MoeLayer(shape_of(cfg, 4), layer.router_w, layer.bias, device=DEV, host_io=True,
                      norm=moe.LayerNorm())
+
+
+@pytest.mark.parametrize("which", ["dense", "experts"])
+def test_buffers_of_a_call_belong_to_its_stream(which):
+    """stream= names a stream that is still busy when the call returns: memory
+    that the current stream takes meanwhile is none of the call's."""
+    moe = _moe()
+    need_gpu()
+    T, d = 300, S.CONFIGS["tiny"].d
+    norm = moe.LayerNorm(1 + rand(d, seed=3, scale=0.1, dt=torch.float32))
+    if which == "dense":
+        run = moe.GatedFfn(rand(512, d, seed=1, scale=d ** -0.5), rand(d, 256, seed=2, scale=0.06), norm)
+    else:
+        run, _ = moe_layer(T, norm=norm)
+    x, dy = rand(T, d, seed=5), rand(T, d, seed=6)
+
+    def step(stream=None):
+        y = run.forward_train(x, keep="fp8", stream=stream)
+        return [y, *run.backward(dy, wgrad=True, stream=stream), norm.dweight, norm.dbias]
+    want = [v.clone() for v in step()]
+    side = torch.cuda.Stream()
+    step(side)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    got = step(side)
+    junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+            for n in [1 << k for k in range(9, 24)] * 8]
+    side.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    del junk
+
+
+def test_in_place_outputs():
+    """y may be x where x itself is not kept, and is refused where it is."""
+    moe = _moe()
+    need_gpu()
+    T, d = 70, 256
+    x, dy = rand(T, d, seed=1), rand(T, d, seed=2)
+    ln = moe.LayerNorm(1 + rand(d, seed=3, scale=0.1, dt=torch.float32))
+    ffn = moe.GatedFfn(rand(512, d, seed=4, scale=d ** -0.5), rand(d, 256, seed=5, scale=0.06), ln)
+    for run in (ln, ffn):
+        want = [run.forward_train(x, keep="fp8")]
+        want += [v.clone() for v in torch.utils._pytree.tree_leaves(run.backward(dy))]
+        z = x.clone()
+        got = [run.forward_train(z, y=z, keep="fp8")]
+        got += torch.utils._pytree.tree_leaves(run.backward(dy))
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+        with pytest.raises(ValueError, match="kept for backward"):
+            run.forward_train(z, y=z, keep="full")
+    with pytest.raises(ValueError, match="kept for backward"):
+        moe.GatedFfn(ffn.w13, ffn.w2).forward_train(z, y=z, keep="fp8")
+    q, s = torch.zeros(4, 256, dtype=torch.int8, device=DEV), torch.zeros(2, 4, device=DEV)
+    with pytest.raises(ValueError, match="dtype"):
+        moe.moe_swiglu_backward_quant_ckpt(torch.zeros(4, 128, device=DEV), q, s, 4, 128, 4, q.view(torch.uint8), s)

@@ -421,3 +421,50 @@ def test_norm_and_checkpoint_on_another_stream_and_in_a_graph():
     torch.cuda.synchronize()
     for k, v in bufs.items():
         assert torch.equal(v, got[k]), k
+
+
+def test_offsets_past_32_bits():
+    """Rows whose elements lie beyond 2^31 give what the same rows give alone."""
+    import fp8_block_scaled_affinity_b200 as moe
+    need_gpu()
+    cols = 7168
+    rows = 2 ** 31 // cols + 700
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x.copy_(rand(1, cols, seed=1).expand(rows, cols))
+    x[-600:] = rand(600, cols, seed=2).bfloat16()
+    w = 1 + 0.1 * rand(cols, seed=3)
+
+    def step(x):
+        n = x.shape[0]
+        y, dx = torch.empty_like(x), torch.empty_like(x)
+        mean, rstd = torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+        moe.moe_layernorm_forward(x, w, None, 1e-5, y, mean, rstd)
+        q, s = pack(moe, x)
+        back = torch.empty_like(x)
+        moe.moe_ckpt_unpack(q, s, back)
+        moe.moe_layernorm_backward(y, q, s, w, mean, rstd, dx, None, None, None)
+        dx2 = torch.empty_like(x)
+        moe.moe_layernorm_backward(y, x, None, w, mean, rstd, dx2, None, None, None)
+        return y[-600:], q[-600:], s[:, -600:], back[-600:], mean[-600:], rstd[-600:], dx[-600:], dx2[-600:]
+    for a, b in zip(step(x), step(x[-600:].clone())):
+        assert torch.equal(a, b)
+
+
+def test_swiglu_backward_offsets_past_32_bits():
+    import fp8_block_scaled_affinity_b200 as moe
+    need_gpu()
+    inter = 2048
+    rows = 2 ** 31 // (2 * inter) + 300
+    ac = torch.zeros(rows, 2 * inter, dtype=torch.uint8, device=DEV)
+    ac[-200:] = torch.randint(0, 0x7F, (200, 2 * inter), device=DEV).to(torch.uint8)
+    s = 0.01 + torch.rand(2 * inter // 128, rows, device=DEV)
+    dh = torch.zeros(rows, inter, device=DEV)
+    dh[-200:] = rand(200, inter, seed=2)
+
+    def step(dh, ac, s):
+        n = dh.shape[0]
+        q, qs = torch.empty_like(ac), torch.empty_like(s)
+        moe.moe_swiglu_backward_quant_ckpt(dh, ac, s, n, inter, n, q, qs)
+        return q[-200:], qs[:, -200:]
+    for a, b in zip(step(dh, ac, s), step(dh[-200:].clone(), ac[-200:].clone(), s[:, -200:].contiguous())):
+        assert torch.equal(a, b)
