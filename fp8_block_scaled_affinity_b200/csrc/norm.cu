@@ -17,7 +17,7 @@
 // registers leave room for one wide row at a time on an SM, whose loads and
 // barrier nothing else hides.  So rows are streamed: several ahead are copied
 // into shared memory in bulk, which goes on whatever the threads wait for
-// (4096 rows of 7168 kept in 8 bits: 53 us, 73 us with each row loaded when
+// (4096 rows of 7168 kept in 8 bits: 47 us, 20 us more with each row loaded when
 // its turn comes).  Rows that are no multiple of 16 bytes are copied from
 // the 16-byte boundary before them, and read an element at a time.
 #include <algorithm>
@@ -222,12 +222,15 @@ __global__ void __launch_bounds__(1024) layernorm_backward_kernel(const T* __res
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
         const int c = (t + j * tpr) * E;
+        if (c < cols) {
+            float a[E], b[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if (c + i < cols) {
-                p[c + i] = dw[j * E + i];
-                p[cols + c + i] = db[j * E + i];
+            for (int i = 0; i < E; ++i) {
+                a[i] = dw[j * E + i];
+                b[i] = db[j * E + i];
             }
+            store_floats(p + c, a);
+            store_floats(p + cols + c, b);
         }
     }
 }
@@ -332,8 +335,8 @@ struct Turn {
 
 // 16 columns a thread in chunks of E: chunk j starts at column (t + j tpr) E.
 // Bound by the instructions of a row and the walk from one barrier to the next,
-// not by memory: 53 us for 4096 rows of 7168 kept in 8 bits, which read and
-// write 150 MB (23 us); 60 us with 8 columns and twice the threads.
+// not by memory: 47 us for 4096 rows of 7168 kept in 8 bits, which read and
+// write 150 MB (23 us); 7 us more with 8 columns and twice the threads.
 template <class T, class X, int E>
 __global__ void __launch_bounds__(kStreamThreads)
     layernorm_backward_stream(const Rows dy, const Rows x, const float* __restrict__ x_scales,
@@ -499,12 +502,15 @@ __global__ void __launch_bounds__(kStreamThreads)
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
         const int c = (t + j * tpr) * E;
+        if (c < cols) {
+            float a[E], b[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            if (c + e < cols) {
-                p[c + e] = reinterpret_cast<float*>(dw)[j * E + e];
-                p[cols + c + e] = reinterpret_cast<float*>(db)[j * E + e];
+            for (int e = 0; e < E; ++e) {
+                a[e] = reinterpret_cast<float*>(dw)[j * E + e];
+                b[e] = reinterpret_cast<float*>(db)[j * E + e];
             }
+            store_floats(p + c, a);
+            store_floats(p + cols + c, b);
         }
     }
 }
@@ -541,14 +547,15 @@ __global__ void __launch_bounds__(1024) layernorm_sum_kernel(const float* __rest
 int stream_threads(int cols) { return ((cols + kPerThread - 1) / kPerThread + 31) / 32 * 32; }
 
 // CTAs of the backward pass: what an SM holds (512 threads of 128 registers),
-// and no more than leave four rows to each (a CTA's partial sums are written
-// and read once, as much as one or two rows).
+// and no more than leave three rows to each (a CTA's partial sums are written
+// and read once, as much as one or two rows; 1001 fp32 rows of 1477: 11.3 us,
+// 12.6 with four rows, 11.6 with two; 1001 bf16 rows of 1480: 8.5, 9.4, 9.9).
 int backward_per_sm(int cols) {
     return std::max(1, std::min(kMaxCtas, kStreamThreads / stream_threads(cols)));
 }
 int backward_ctas(int64_t rows, int cols) {
     const int64_t most = int64_t(sm_count()) * backward_per_sm(cols);
-    return int(std::min(rows, std::min(most, std::max<int64_t>(sm_count(), rows / 4))));
+    return int(std::min(rows, std::min(most, std::max<int64_t>(sm_count(), rows / 3))));
 }
 
 // Rows ahead for `ctas` CTAs an SM and rows of `slot` bytes: two at least
