@@ -283,17 +283,29 @@ __device__ __forceinline__ float sigmoid_fast(float a) {
     return __fdividef(1.0f, 1.0f + __expf(-a));
 }
 
+// da, dc and h of one feature from dh and the kept a and c.
+__device__ __forceinline__ void gated_backward(float dh, float a, float c, float& da, float& dc,
+                                               float& h) {
+    const float s = sigmoid_fast(a);
+    const float as = a * s, ds = dh * s;
+    h = as * c;
+    dc = dh * as;
+    da = ds * c * fmaf(a, 1.0f - s, 1.0f);
+}
+
+// 4 values -> their codes
+__device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
+    return e4m3x2(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv)) |
+           (uint32_t(e4m3x2(__fmul_rn(v[2], inv), __fmul_rn(v[3], inv))) << 16);
+}
+
 // 32 values -> 32 codes at q (32-byte aligned)
 __device__ __forceinline__ void put_codes(uint8_t* q, const float (&v)[32], float inv) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float* f = v + 16 * j + 4 * i;
-            w[i] = e4m3x2(__fmul_rn(f[0], inv), __fmul_rn(f[1], inv)) |
-                   (uint32_t(e4m3x2(__fmul_rn(f[2], inv), __fmul_rn(f[3], inv))) << 16);
-        }
+        for (int i = 0; i < 4; ++i) w[i] = codes4(v + 16 * j + 4 * i, inv);
         reinterpret_cast<uint4*>(q)[j] = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
@@ -466,14 +478,9 @@ __device__ __forceinline__ void epilogue(const Args& a, Shared* ss, char* park_a
                     kept_floats<T, KEPT>(kept.a, j, kept.sa, ka);
                     kept_floats<T, KEPT>(kept.c, j, kept.sc, kc);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float dh = __uint_as_float(v[8 * j + i]);
-                        const float s = sigmoid_fast(ka[i]);
-                        const float as = ka[i] * s, ds = dh * s;
-                        h[8 * j + i] = as * kc[i];
-                        dc[8 * j + i] = dh * as;
-                        da[8 * j + i] = ds * kc[i] * fmaf(ka[i], 1.0f - s, 1.0f);
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        gated_backward(__uint_as_float(v[8 * j + i]), ka[i], kc[i], da[8 * j + i],
+                                       dc[8 * j + i], h[8 * j + i]);
                 }
                 const bool any = rows_any && x < a.inter;
                 put32<T, BOXES>(da, park, box, &p.out, x, y0, any);
@@ -551,8 +558,14 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
 
 // ================================================== few tokens: split K
 // out[t, r] = sum_k W[r, k] x[t, k] for 128 rows r of W a CTA: W is the M side
-// of the MMA (a row per TMEM lane), nt tokens the N side.  GATED: 64 rows of
-// W1 in lanes 0-63 and the same 64 of W3 in lanes 64-127.
+// of the MMA (a row per TMEM lane), nt tokens the N side.
+//   kFewPlain     the product
+//   kFewTurned    the same with W as [k, r] in memory, read as it lies (dx)
+//   kFewGated     64 rows of W1 in lanes 0-63 and the same 64 of W3 in lanes
+//                 64-127: h
+//   kFewKept      the same, and a and c kept; two CTAs of the cluster have the
+//                 128 features of a tile between them
+//   kFewBackward  W2 as [k, r]: dh, and from it and the kept a, c: da, dc, h
 //   warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 move the accumulator
 //   into shared memory (over the stages, all consumed by then); then every
 //   CTA of the cluster adds up its share of the tokens, ranks in order.
@@ -564,15 +577,22 @@ constexpr int kFewShared = 64;         // tokens up to which two share an SM
 constexpr int kFewMaxTokens = 256;  // N side of one tile
 constexpr int kFewMaxSplit = 8;     // portable cluster size
 
+enum FewMode { kFewPlain, kFewTurned, kFewGated, kFewKept, kFewBackward };
+constexpr bool few_gated(int mode) { return mode == kFewGated || mode == kFewKept; }
+constexpr bool few_turned(int mode) { return mode == kFewTurned || mode == kFewBackward; }
+
 struct FewArgs {
     CUtensorMap w, x;
-    void* out;
+    void* out;      // kFewBackward: [da | dc]
+    void* h;        // kFewBackward
+    void* ac;       // kFewKept (out), kFewBackward (in)
+    float* ac_scales;
+    int kept;
     int rows;       // output columns (W2's rows, or features)
     int pitch;      // of out
     int w3;         // GATED: first row of W3
     int64_t tokens;
     int nt;         // tokens of a tile, a multiple of 16
-    int tiles_w;
     int nkb;
     int ring;       // bytes of the stages
     int stages;
@@ -594,13 +614,47 @@ static_assert(kFewMaxTokens * 128 * 4 <= kFewRing1 && kFewShared * 128 * 4 <= kF
 static_assert(few_smem(kFewRing1) <= 232448 && 2 * (few_smem(kFewRing2) + 1024) <= 233472,
               "shared memory of an SM");
 
+// Two neighbouring features' kept a and c of one token.
+template <class T>
+struct KeptPair {
+    uint32_t a, c;
+    float sa, sc;
+    __device__ __forceinline__ void load(const FewArgs& g, int64_t t, int f) {
+        a = c = 0u;
+        sa = sc = 0.0f;
+        if (f >= g.rows) return;
+        if (g.kept == kKept8) {
+            const int64_t wide = (g.rows + kTile - 1) / kTile * kTile;
+            const uint8_t* q = static_cast<const uint8_t*>(g.ac) + t * 2 * wide + f;
+            a = __ldg(reinterpret_cast<const uint16_t*>(q));
+            c = __ldg(reinterpret_cast<const uint16_t*>(q + wide));
+            sa = __ldg(g.ac_scales + int64_t(f / kTile) * g.tokens + t);
+            sc = __ldg(g.ac_scales + (wide / kTile + f / kTile) * g.tokens + t);
+        } else {
+            const T* q = static_cast<const T*>(g.ac) + t * 2 * g.rows + f;
+            a = __ldg(reinterpret_cast<const uint32_t*>(q));
+            c = __ldg(reinterpret_cast<const uint32_t*>(q + g.rows));
+        }
+    }
+    __device__ __forceinline__ void get(const FewArgs& g, float2& va, float2& vc) const {
+        if (g.kept == kKept8) {
+            va = mul2(e4m3x2_to_float2(uint16_t(a)), both(sa));
+            vc = mul2(e4m3x2_to_float2(uint16_t(c)), both(sc));
+        } else {
+            unpack2f(T(), a, va.x, va.y);
+            unpack2f(T(), c, vc.x, vc.y);
+        }
+    }
+};
+
 // The sums of this CTA's share of the tile over the cluster's partial sums,
 // ranks in order, and the output.  A warp takes 64 columns of a token at a
 // time, two a lane; eight ranks' loads, or several tokens' of fewer ranks, are
 // in flight together.
-template <bool GATED, class T, int SPLIT>
+template <int MODE, class T, int SPLIT>
 __device__ __forceinline__ void few_sum(const FewArgs& a, uint32_t part, int rank, int wt,
                                         int64_t t0) {
+    constexpr bool GATED = few_gated(MODE);
     constexpr int kBatch = 8 / SPLIT;
     constexpr int kSteps = GATED ? 1 : 2;  // pieces of 64 output columns
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -612,10 +666,13 @@ __device__ __forceinline__ void few_sum(const FewArgs& a, uint32_t part, int ran
     for (int k = 0; k < SPLIT; ++k) at[k] = mapa(part, k) + uint32_t(lane) * 8u;
     for (int i0 = rank + SPLIT * warp; i0 < items; i0 += kBatch * step) {
         float2 v[kBatch][SPLIT], u[kBatch][SPLIT];
+        KeptPair<T> kept[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const int i = i0 + j * step;
             if (i < items) {
+                if constexpr (MODE == kFewBackward)
+                    kept[j].load(a, t0 + i / kSteps, wt * 128 + 64 * (i % kSteps) + 2 * lane);
                 const uint32_t off = uint32_t((i / kSteps) * 128 + 64 * (i % kSteps)) * 4u;
 #pragma unroll
                 for (int k = 0; k < SPLIT; ++k) {
@@ -645,26 +702,122 @@ __device__ __forceinline__ void few_sum(const FewArgs& a, uint32_t part, int ran
                     s.x = s.x * sigmoid_fast(s.x) * c.x;
                     s.y = s.y * sigmoid_fast(s.y) * c.y;
                 }
-                *reinterpret_cast<uint32_t*>(out + (t0 + i / kSteps) * a.pitch + r) =
-                    pack2t(T(), s.x, s.y);
+                T* const o = out + (t0 + i / kSteps) * a.pitch + r;
+                if constexpr (MODE == kFewBackward) {
+                    float2 ka, kc, da, dc, h;
+                    kept[j].get(a, ka, kc);
+                    gated_backward(s.x, ka.x, kc.x, da.x, dc.x, h.x);
+                    gated_backward(s.y, ka.y, kc.y, da.y, dc.y, h.y);
+                    s = da;
+                    *reinterpret_cast<uint32_t*>(o + a.rows) = pack2t(T(), dc.x, dc.y);
+                    *reinterpret_cast<uint32_t*>(static_cast<T*>(a.h) +
+                                                 (t0 + i / kSteps) * a.rows + r) =
+                        pack2t(T(), h.x, h.y);
+                }
+                *reinterpret_cast<uint32_t*>(o) = pack2t(T(), s.x, s.y);
             }
         }
     }
 }
 
-template <bool GATED, class T>
+// The same for kFewKept: a warp takes the 128 features of a token, four a
+// lane, from the two CTAs that have them (even and odd ranks), and keeps a
+// and c as the pairs' epilogue does.
+template <class T, int SPLIT>
+__device__ __forceinline__ void few_keep(const FewArgs& a, uint32_t part, int rank, int tile,
+                                         int64_t t0) {
+    constexpr int kBatch = 4 / SPLIT;
+    constexpr int step = 2 * SPLIT * (kFewThreads / 32);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int items = int(min(int64_t(a.nt), a.tokens - t0));
+    const int f = tile * kTile + 4 * lane;
+    const bool have = f < a.rows;  // a multiple of 8: four features exist together
+    const int64_t wide = (a.rows + kTile - 1) / kTile * kTile;
+    T* const out = static_cast<T*>(a.out);
+    uint32_t at[SPLIT];
+#pragma unroll
+    for (int k = 0; k < SPLIT; ++k)
+        at[k] = mapa(part, 2 * k + (lane >> 4)) + uint32_t(lane & 15) * 16u;
+    for (int i0 = rank + 2 * SPLIT * warp; i0 < items; i0 += kBatch * step) {
+        float4 v[kBatch][SPLIT], u[kBatch][SPLIT];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * step;
+            if (i < items) {
+#pragma unroll
+                for (int k = 0; k < SPLIT; ++k) {
+                    v[j][k] = ld_cluster4(at[k] + uint32_t(i) * 512u);
+                    u[j][k] = ld_cluster4(at[k] + uint32_t(i) * 512u + 256u);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * step;
+            if (i >= items) break;
+            float s[4] = {v[j][0].x, v[j][0].y, v[j][0].z, v[j][0].w};
+            float c[4] = {u[j][0].x, u[j][0].y, u[j][0].z, u[j][0].w};
+#pragma unroll
+            for (int k = 1; k < SPLIT; ++k) {
+                s[0] += v[j][k].x, s[1] += v[j][k].y, s[2] += v[j][k].z, s[3] += v[j][k].w;
+                c[0] += u[j][k].x, c[1] += u[j][k].y, c[2] += u[j][k].z, c[3] += u[j][k].w;
+            }
+            const int64_t t = t0 + i;
+            if (a.kept == kKept8) {
+                float ma = 0.0f, mc = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // columns past the last feature (rows of W3 for a) are kept as zeros
+                    if (!have) s[e] = c[e] = 0.0f;
+                    ma = fmaxf(ma, fabsf(s[e]));
+                    mc = fmaxf(mc, fabsf(c[e]));
+                }
+                // as integers, whose order is that of values that are not negative
+                ma = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(ma)));
+                mc = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mc)));
+                float sa, sc, ia, ic;
+                kept_scale(ma, sa, ia);
+                kept_scale(mc, sc, ic);
+                uint8_t* const q = static_cast<uint8_t*>(a.ac) + t * 2 * wide + f;
+                *reinterpret_cast<uint32_t*>(q) = codes4(s, ia);
+                *reinterpret_cast<uint32_t*>(q + wide) = codes4(c, ic);
+                if (lane == 0) {
+                    a.ac_scales[int64_t(tile) * a.tokens + t] = sa;
+                    a.ac_scales[(wide / kTile + tile) * a.tokens + t] = sc;
+                }
+            } else if (have) {
+                T* const q = static_cast<T*>(a.ac) + t * 2 * a.rows + f;
+                *reinterpret_cast<uint2*>(q) =
+                    make_uint2(pack2t(T(), s[0], s[1]), pack2t(T(), s[2], s[3]));
+                *reinterpret_cast<uint2*>(q + a.rows) =
+                    make_uint2(pack2t(T(), c[0], c[1]), pack2t(T(), c[2], c[3]));
+            }
+            if (have) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] = s[e] * sigmoid_fast(s[e]) * c[e];
+                *reinterpret_cast<uint2*>(out + t * a.rows + f) =
+                    make_uint2(pack2t(T(), s[0], s[1]), pack2t(T(), s[2], s[3]));
+            }
+        }
+    }
+}
+
+template <int MODE, class T>
 __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewArgs a) {
+    constexpr bool GATED = few_gated(MODE), MN = few_turned(MODE), KEPT = MODE == kFewKept;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     FewShared* ss = reinterpret_cast<FewShared*>(smem + a.ring);
     const int warp = int(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const int rank = blockIdx.x, split = gridDim.x;  // the cluster is the x row of the grid
-    const int wt = blockIdx.y;
+    // the cluster is the x row of the grid
+    const int rank = blockIdx.x, split = KEPT ? gridDim.x / 2 : gridDim.x;
+    const int kr = KEPT ? rank / 2 : rank;
+    const int wt = KEPT ? 2 * blockIdx.y + (rank & 1) : blockIdx.y;
     const int64_t t0 = int64_t(blockIdx.z) * a.nt;
     // this CTA's part of K
-    const int kb0 = int(int64_t(a.nkb) * rank / split);
-    const int n = int(int64_t(a.nkb) * (rank + 1) / split) - kb0;
+    const int kb0 = int(int64_t(a.nkb) * kr / split);
+    const int n = int(int64_t(a.nkb) * (kr + 1) / split) - kb0;
     const uint32_t cols = a.nt <= 32 ? 32 : a.nt <= 64 ? 64 : a.nt <= 128 ? 128 : 256;
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
@@ -695,8 +848,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             const uint32_t bar = smem_u32(&ss->full[s]);
             const uint32_t dst = smem_u32(smem) + s * stage_bytes;
             mbar_arrive_expect_tx(bar, uint32_t(stage_bytes));
-            tma_load_2d(dst, &a.w, bar, k0, w0);
-            if (GATED) tma_load_2d(dst + kOperandBytes / 2, &a.w, bar, k0, a.w3 + w0);
+            if (MN) {
+                tma_load_2d(dst, &a.w, bar, w0, k0);
+                tma_load_2d(dst + kPieceBytes, &a.w, bar, w0 + 64, k0);
+            } else {
+                tma_load_2d(dst, &a.w, bar, k0, w0);
+                if (GATED) tma_load_2d(dst + kOperandBytes / 2, &a.w, bar, k0, a.w3 + w0);
+            }
         };
         auto load_x = [&](int i, int s) {
             tma_load_2d(smem_u32(smem) + s * stage_bytes + kOperandBytes, &a.x,
@@ -733,8 +891,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                              quiesce_ns(a.wait_limit_ns));
     } else if (warp == 1) {
         const bool lead = elect_one();
-        const uint32_t idesc = idesc_f16(std::is_same<T, bf16_t>::value, 0, 0, 128, a.nt);
-        const uint64_t desc0 = sw128_desc16(smem_u32(smem), 16);
+        const uint32_t idesc = idesc_f16(std::is_same<T, bf16_t>::value, MN, 0, 128, a.nt);
+        constexpr uint32_t w_step = MN ? 2048 / 16 : 32 / 16;  // as in the pairs' issuer
+        const uint64_t desc0 = sw128_desc16(smem_u32(smem), kPieceBytes);
         int s = 0;
         uint32_t par = 0;
         for (int i = 0; i < n; ++i) {
@@ -748,7 +907,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             if (lead) {
 #pragma unroll
                 for (int kk = 0; kk < kTileK / 16; ++kk)
-                    mma_f16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (i | kk) ? 1u : 0u);
+                    mma_f16(tmem, ad + w_step * kk, bd + 2 * kk, idesc, (i | kk) ? 1u : 0u);
                 commit(smem_u32(&ss->empty[s]));
             }
             __syncwarp();
@@ -784,10 +943,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     }
     cluster_sync();  // every CTA's partial sums are in place
     if (!bad) {
-        if (split == 1) few_sum<GATED, T, 1>(a, smem_u32(part), rank, wt, t0);
-        else if (split == 2) few_sum<GATED, T, 2>(a, smem_u32(part), rank, wt, t0);
-        else if (split == 4) few_sum<GATED, T, 4>(a, smem_u32(part), rank, wt, t0);
-        else few_sum<GATED, T, 8>(a, smem_u32(part), rank, wt, t0);
+        if constexpr (KEPT) {
+            if (split == 1) few_keep<T, 1>(a, smem_u32(part), rank, blockIdx.y, t0);
+            else if (split == 2) few_keep<T, 2>(a, smem_u32(part), rank, blockIdx.y, t0);
+            else few_keep<T, 4>(a, smem_u32(part), rank, blockIdx.y, t0);
+        } else {
+            if (split == 1) few_sum<MODE, T, 1>(a, smem_u32(part), rank, wt, t0);
+            else if (split == 2) few_sum<MODE, T, 2>(a, smem_u32(part), rank, wt, t0);
+            else if (split == 4) few_sum<MODE, T, 4>(a, smem_u32(part), rank, wt, t0);
+            else few_sum<MODE, T, 8>(a, smem_u32(part), rank, wt, t0);
+        }
     }
     cluster_sync();  // nobody's partial sums are read any more
     if (warp == 1) {
@@ -966,7 +1131,8 @@ struct Maker {
 // The columns of a launch's pair tiles, and about how long it takes, in SM
 // clocks.  A stage of 64 K elements takes the MMA 2 clocks a column, and 100
 // more; a column of the epilogue costs `epilogue` clocks, under the next
-// tile's products but for the last tile's; starting and ending take 5500.  So
+// tile's products but for the last tile's; starting and ending take 5500; and
+// no launch ends before its longest tile.  So
 // few tiles are cut narrow (256 tokens, d = 512, inter = 256: dy W2 14 us in one
 // tile of 256 columns, 9 us in four of 64), and many take the width whose
 // rounds over the pairs waste least (4096 x 7168 on 74 pairs: 7 rounds of 256
@@ -981,21 +1147,25 @@ struct Extent {
     int64_t m, n;
     int nkb;
 };
+constexpr int64_t kLaunchClocks = 5500;
 PairPlan pair_plan(const Extent* e, int count, int epilogue, std::initializer_list<int> widths) {
     const int pairs = std::max(1, sm_count() / 2);
     PairPlan best;
     for (int nt : widths) {
-        int64_t tiles = 0, main = 0;
+        int64_t tiles = 0, main = 0, longest = 0;
         for (int i = 0; i < count; ++i) {
             const int64_t t = (e[i].m + kTileM - 1) / kTileM * ((e[i].n + nt - 1) / nt);
             tiles += t;
             main += t * e[i].nkb * (2 * nt + 100);
+            if (t > 0) longest = std::max<int64_t>(longest, e[i].nkb * (2 * nt + 100));
         }
         if (tiles == 0) return PairPlan{256, 0};
         main /= tiles;  // of an average tile
         const int64_t epi = int64_t(epilogue) * nt;
         const int64_t clocks =
-            5500 + (tiles + pairs - 1) / pairs * std::max(main, epi) + std::min(main, epi);
+            kLaunchClocks +
+            std::max(longest, (tiles + pairs - 1) / pairs * std::max(main, epi)) +
+            std::min(main, epi);
         if (clocks < best.clocks) {
             best.nt = nt;
             best.clocks = clocks;
@@ -1036,35 +1206,6 @@ Args make_args(int64_t T, int inter, int* dev_status) {
     return a;
 }
 
-template <class T>
-int backward(Maker mk, const void* dy, const void* x, const void* w13, const void* w2, void* ac,
-             int kept, const float* ac_scales, int64_t rows, int d, int I, void* dac, void* h,
-             void* dx, void* dw13, void* dw2, int* dev_status, cudaStream_t st) {
-    Args a = make_args(rows, I, dev_status);
-    a.ac = ac;
-    a.ac_scales = const_cast<float*>(ac_scales);
-    const int kd = (d + kTileK - 1) / kTileK, kt = int((rows + kTileK - 1) / kTileK);
-    const Extent ea = {rows, I, kd};
-    product(a, mk, dy, false, w2, true, h, rows, I, d,
-            pair_plan(&ea, 1, kBackwardClocks, {256, 128, 64}).nt);
-    mk.output(&a.p[0].out, dac, rows, I, 2 * int64_t(I));
-    mk.output(&a.o1, static_cast<uint16_t*>(dac) + I, rows, I, 2 * int64_t(I));
-    mk.output(&a.o2, h, rows, I, I);
-    Args b = make_args(rows, I, dev_status);
-    const Extent eb[3] = {{dx ? rows : 0, d, (2 * I + kTileK - 1) / kTileK},
-                          {dw13 ? 2 * int64_t(I) : 0, d, kt},
-                          {dw2 ? d : 0, I, kt}};
-    const int nt = pair_plan(eb, 3, kPlainClocks, {256, 128, 64}).nt;
-    if (dx) product(b, mk, dac, false, w13, true, dx, rows, d, 2 * int64_t(I), nt);
-    if (dw13) product(b, mk, dac, true, x, true, dw13, 2 * int64_t(I), d, rows, nt);
-    if (dw2) product(b, mk, dy, true, h, true, dw2, d, I, rows, nt);
-    b.wait_first = 1;
-    if (!mk.ok) return MOE_ERR_CUDA;
-    const int rc = kept == kKept8 ? launch<kBackward, kKept8, T>(a, st)
-                                  : launch<kBackward, kKept16, T>(a, st);
-    return rc != MOE_OK || b.n_problems == 0 ? rc : launch<kPlain, kKeptNone, T>(b, st);
-}
-
 // How a product with few tokens is laid out, and about how long it takes, in
 // SM clocks fitted to 12 sizes from 16 to 1024 tokens, d and inter from 512 to
 // 7168 and 256 to 2048: for 64 K elements 3 clocks a token (the MMA's 2, and
@@ -1074,11 +1215,14 @@ struct FewPlan {
     int tiles_t, tiles_w, nt, split, ring;
     int64_t clocks;
 };
-FewPlan few_plan(int64_t T, int rows, int rows_per_tile, int nkb) {
+FewPlan few_plan(int mode, int64_t T, int rows, int nkb) {
+    const int rows_per_tile = few_gated(mode) ? 64 : 128;
+    const int max_split = mode == kFewKept ? kFewMaxSplit / 2 : kFewMaxSplit;
     FewPlan p;
     p.tiles_t = int((T + kFewMaxTokens - 1) / kFewMaxTokens);
     p.nt = int(((T + p.tiles_t - 1) / p.tiles_t + 15) / 16 * 16);
     p.tiles_w = (rows + rows_per_tile - 1) / rows_per_tile;
+    if (mode == kFewKept) p.tiles_w += p.tiles_w & 1;
     const int64_t tiles = int64_t(p.tiles_t) * p.tiles_w;
     const int sms = sm_count();
     // Up to 64 tokens two CTAs share an SM, so that one fetches while the
@@ -1089,7 +1233,7 @@ FewPlan few_plan(int64_t T, int rows, int rows_per_tile, int nkb) {
     const bool two = p.nt <= kFewShared;
     p.ring = two ? kFewRing2 : kFewRing1;
     p.split = 1;
-    while (p.split < kFewMaxSplit && tiles * p.split * 4 < int64_t(sms) * (two ? 4 : 3) &&
+    while (p.split < max_split && tiles * p.split * 4 < int64_t(sms) * (two ? 4 : 3) &&
            nkb >= 8 * p.split)
         p.split *= 2;
     const int64_t waves = (tiles * p.split + sms - 1) / sms;
@@ -1098,7 +1242,9 @@ FewPlan few_plan(int64_t T, int rows, int rows_per_tile, int nkb) {
     return p;
 }
 // Whether a plan beats pairs: only where tiles of 256 x 256 leave pairs idle,
-// and then by the two estimates.
+// and then by the two estimates.  (Forward that keeps a and c, and backward: 48
+// tokens, d = 1032, inter = 328 24.8 us, all in pairs 31.6; 300 tokens, d = 4104,
+// inter = 136 41 and 75 us; 16 tokens, d = 7168, inter = 2048 87 and 118 us.)
 bool few_better(const FewPlan& p, int64_t m, int64_t n, const PairPlan& pair) {
     return (m + kTileM - 1) / kTileM * ((n + 255) / 256) < sm_count() / 2 &&
            p.clocks < pair.clocks;
@@ -1135,44 +1281,57 @@ int launch_vec(const void* w, const void* x, void* out, int tokens, int rows, in
                          : launch_vec_tok<GATED, 4, T>(w, x, out, tokens, rows, K, after, st);
 }
 
-template <bool GATED, class T>
+// kept, ac, ac_scales, h: kFewKept and kFewBackward.
+struct FewKept {
+    void* ac;
+    float* ac_scales;
+    int kept;
+    void* h;
+};
+template <int MODE, class T>
 int launch_few(Maker& mk, const FewPlan& p, const void* w, const void* x, void* out, int64_t tokens,
-               int rows, int K, int* dev_status, bool after, cudaStream_t st) {
+               int rows, int K, const FewKept& kept, int* dev_status, bool after,
+               cudaStream_t st) {
     FewArgs a = {};
-    mk.operand(&a.w, w, GATED ? 2 * int64_t(rows) : rows, K, GATED ? 64 : 128);
+    if (few_turned(MODE)) mk.operand(&a.w, w, K, rows, 64);
+    else mk.operand(&a.w, w, few_gated(MODE) ? 2 * int64_t(rows) : rows, K, few_gated(MODE) ? 64 : 128);
     mk.operand(&a.x, x, tokens, K, p.nt);
     if (!mk.ok) return MOE_ERR_CUDA;
     a.out = out;
+    a.h = kept.h;
+    a.ac = kept.ac;
+    a.ac_scales = kept.ac_scales;
+    a.kept = kept.kept;
     a.rows = rows;
-    a.pitch = rows;
+    a.pitch = MODE == kFewBackward ? 2 * rows : rows;
     a.w3 = rows;
     a.tokens = tokens;
     a.nt = p.nt;
-    a.tiles_w = p.tiles_w;
     a.nkb = (K + kTileK - 1) / kTileK;
     a.ring = p.ring;
     a.stages = std::min(kFewMaxStages, p.ring / (kOperandBytes + p.nt * 128));
     a.wait_first = after;
     a.dev_status = dev_status;
     a.wait_limit_ns = wait_limit_ns();
-    if (cudaFuncSetAttribute(few_kernel<GATED, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(few_kernel<MODE, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(few_smem(p.ring))) != cudaSuccess)
         return MOE_ERR_CUDA;
+    const int pair = MODE == kFewKept ? 2 : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(p.split), unsigned(p.tiles_w), unsigned(p.tiles_t));
+    cfg.gridDim = dim3(unsigned(pair * p.split), unsigned(p.tiles_w / pair), unsigned(p.tiles_t));
     cfg.blockDim = dim3(kFewThreads, 1, 1);
     cfg.dynamicSmemBytes = few_smem(p.ring);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(p.split);
+    attr[0].val.clusterDim.x = cfg.gridDim.x;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = after ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, few_kernel<GATED, T>, a) != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, few_kernel<MODE, T>, a) != cudaSuccess) return MOE_ERR_CUDA;
     return check_launch();
 }
 
@@ -1182,14 +1341,15 @@ int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t ro
             cudaStream_t st) {
     const int kd = (d + kTileK - 1) / kTileK, ki = (I + kTileK - 1) / kTileK;
     // few tokens: whichever way takes fewer clocks.  (One token, d = 7168,
-    // inter = 2048: 70 us in pairs of CTAs.)  What is kept comes from the pairs'
-    // epilogue, and in 8 bits from tiles that see 128 features together.
+    // inter = 2048: 70 us in pairs of CTAs.)  a and c are kept in 8 bits from
+    // tiles that see 128 features together.
     const Extent ea = {rows, 2 * int64_t(I), kd}, eb = {rows, d, ki};
     const PairPlan pa = kept == kKept8 ? pair_plan(&ea, 1, kGatedClocks, {256})
                                        : pair_plan(&ea, 1, kGatedClocks, {256, 128});
     const PairPlan pb = pair_plan(&eb, 1, kPlainClocks, {256, 224, 192, 160, 128, 96, 64});
-    const FewPlan fa = few_plan(rows, I, 64, kd), fb = few_plan(rows, d, 128, ki);
-    const bool few_a = kept == kKeptNone && few_better(fa, rows, 2 * int64_t(I), pa);
+    const FewPlan fa = few_plan(kept == kKeptNone ? kFewGated : kFewKept, rows, I, kd);
+    const FewPlan fb = few_plan(kFewPlain, rows, d, ki);
+    const bool few_a = few_better(fa, rows, 2 * int64_t(I), pa);
     const bool few_b = few_better(fb, rows, d, pb);
     int rc;
     // One token, or a few with few weights (a token's multiplications cost as
@@ -1201,9 +1361,13 @@ int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t ro
         return rc != MOE_OK ? rc : launch_vec<false, T>(w2, h, y, int(rows), d, I, true, st);
     }
     if (few_a) {
-        rc = launch_few<true, T>(mk, fa, w13, x, h, rows, I, d, dev_status, false, st);
+        rc = kept == kKeptNone
+                 ? launch_few<kFewGated, T>(mk, fa, w13, x, h, rows, I, d, {}, dev_status, false, st)
+                 : launch_few<kFewKept, T>(mk, fa, w13, x, h, rows, I, d, {ac, ac_scales, kept, nullptr},
+                                           dev_status, false, st);
         if (rc != MOE_OK) return rc;
-        if (few_b) return launch_few<false, T>(mk, fb, w2, h, y, rows, d, I, dev_status, true, st);
+        if (few_b)
+            return launch_few<kFewPlain, T>(mk, fb, w2, h, y, rows, d, I, {}, dev_status, true, st);
     }
     Args a = make_args(rows, I, dev_status);
     product(a, mk, x, false, w13, false, h, rows, 2 * int64_t(I), d, pa.nt);
@@ -1229,8 +1393,57 @@ int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t ro
                                : launch<kGated, kKeptNone, T>(a, st);
         if (rc != MOE_OK) return rc;
     }
-    return few_b ? launch_few<false, T>(mk, fb, w2, h, y, rows, d, I, dev_status, true, st)
+    return few_b ? launch_few<kFewPlain, T>(mk, fb, w2, h, y, rows, d, I, {}, dev_status, true, st)
                  : launch<kPlain, kKeptNone, T>(b, st);
+}
+
+template <class T>
+int backward(Maker mk, const void* dy, const void* x, const void* w13, const void* w2, void* ac,
+             int kept, float* ac_scales, int64_t rows, int d, int I, void* dac, void* h, void* dx,
+             void* dw13, void* dw2, int* dev_status, cudaStream_t st) {
+    const int kd = (d + kTileK - 1) / kTileK, kt = int((rows + kTileK - 1) / kTileK);
+    const int k2 = (2 * I + kTileK - 1) / kTileK;
+    // dy W2 and its element-wise step, and dx, with few tokens: as in the
+    // forward pass.  (dx costs a launch of its own then; the choice does not
+    // depend on what else is wanted, so neither do its bits.)
+    const Extent ea = {rows, I, kd}, ex = {rows, d, k2};
+    const PairPlan pa = pair_plan(&ea, 1, kBackwardClocks, {256, 128, 64});
+    const PairPlan px = pair_plan(&ex, 1, kPlainClocks, {256, 128, 64});
+    const FewPlan fa = few_plan(kFewBackward, rows, I, kd);
+    FewPlan fx = few_plan(kFewTurned, rows, d, k2);
+    fx.clocks += kLaunchClocks;
+    const bool few_x = dx && few_better(fx, rows, d, px);
+    int rc;
+    if (few_better(fa, rows, I, pa)) {
+        rc = launch_few<kFewBackward, T>(mk, fa, w2, dy, dac, rows, I, d,
+                                         {ac, ac_scales, kept, h}, dev_status, false, st);
+    } else {
+        Args a = make_args(rows, I, dev_status);
+        a.ac = ac;
+        a.ac_scales = ac_scales;
+        product(a, mk, dy, false, w2, true, h, rows, I, d, pa.nt);
+        mk.output(&a.p[0].out, dac, rows, I, 2 * int64_t(I));
+        mk.output(&a.o1, static_cast<uint16_t*>(dac) + I, rows, I, 2 * int64_t(I));
+        mk.output(&a.o2, h, rows, I, I);
+        if (!mk.ok) return MOE_ERR_CUDA;
+        rc = kept == kKept8 ? launch<kBackward, kKept8, T>(a, st)
+                            : launch<kBackward, kKept16, T>(a, st);
+    }
+    if (rc == MOE_OK && few_x)
+        rc = launch_few<kFewTurned, T>(mk, fx, w13, dac, dx, rows, d, 2 * I, {}, dev_status, true,
+                                       st);
+    if (rc != MOE_OK) return rc;
+    Args b = make_args(rows, I, dev_status);
+    const Extent eb[3] = {{dx && !few_x ? rows : 0, d, k2},
+                          {dw13 ? 2 * int64_t(I) : 0, d, kt},
+                          {dw2 ? d : 0, I, kt}};
+    const int nt = pair_plan(eb, 3, kPlainClocks, {256, 128, 64}).nt;
+    if (dx && !few_x) product(b, mk, dac, false, w13, true, dx, rows, d, 2 * int64_t(I), nt);
+    if (dw13) product(b, mk, dac, true, x, true, dw13, 2 * int64_t(I), d, rows, nt);
+    if (dw2) product(b, mk, dy, true, h, true, dw2, d, I, rows, nt);
+    b.wait_first = 1;
+    if (!mk.ok) return MOE_ERR_CUDA;
+    return b.n_problems == 0 ? MOE_OK : launch<kPlain, kKeptNone, T>(b, st);
 }
 
 int check_sizes(int type, int64_t T, int d, int inter) {
@@ -1301,7 +1514,7 @@ extern "C" MOE_API int moe_ffn_backward(const void* dy, const void* x, const voi
     if (!device_is_sm100()) return MOE_ERR_DEVICE;
     return type == MOE_T_BF16
                ? backward<bf16_t>(maker(type), dy, x, w13, w2, const_cast<void*>(ac), kept,
-                                  ac_scales, T, d, inter, dac, h, dx, dw13, dw2, dev_status, st)
+                                  const_cast<float*>(ac_scales), T, d, inter, dac, h, dx, dw13, dw2, dev_status, st)
                : backward<f16_t>(maker(type), dy, x, w13, w2, const_cast<void*>(ac), kept,
-                                 ac_scales, T, d, inter, dac, h, dx, dw13, dw2, dev_status, st);
+                                 const_cast<float*>(ac_scales), T, d, inter, dac, h, dx, dw13, dw2, dev_status, st);
 }

@@ -87,6 +87,12 @@ def test_forward(T, d, I, t, keep):
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
     moe.moe_ffn_forward(c.x, c.w13, c.w2, h, y, ac, s, dev_status=st)
     assert int(st) == 0
+    assert (y_all[T:] == 7).all() and (h_all[T:] == 7).all()
+    check_forward(c, h, y, ac, s, keep)
+
+
+def check_forward(c, h, y, ac, s, keep):
+    T, I = c.x.shape[0], c.I
     A, ea = prod(c.x, c.w13[:I])
     C, ec = prod(c.x, c.w13[I:])
     H = A * torch.sigmoid(A) * C
@@ -97,7 +103,6 @@ def test_forward(T, d, I, t, keep):
     ty = spread(th, c.w2) + ey
     ty = ty + rnd(c.dt, Y.abs() + ty)
     assert ((y.double() - Y).abs() <= ty).all()
-    assert (y_all[T:] == 7).all() and (h_all[T:] == 7).all()
     if keep == "full":
         ref, e = torch.cat([A, C], 1), torch.cat([ea, ec], 1)
         assert ((ac.double() - ref).abs() <= e + rnd(c.dt, ref.abs() + e)).all()
@@ -131,6 +136,23 @@ def backward_ref(c, A, C):
     return dac, e + rnd(c.dt, dac.abs() + e), H, rnd(c.dt, H) + 4e-6 * H.abs()
 
 
+def check_backward(c, A, C, dac, h, dx, dw13, dw2):
+    DAC, td, H, th = backward_ref(c, A, C)
+    assert ((dac.double() - DAC).abs() <= td).all()
+    assert ((h.double() - H).abs() <= th).all()
+    for got, (a, ta), b in ((dx, (DAC, td), c.w13.t()), (dw13, (DAC.t(), td.t()), c.x.t())):
+        if got is None:
+            continue
+        ref, e = prod(a, b)
+        tol = e + spread(ta, b)
+        assert ((got.double() - ref).abs() <= tol + rnd(c.dt, ref.abs() + tol)).all()
+    if dw2 is None:
+        return
+    ref, e = prod(c.dy.t(), H.t())
+    tol = e + spread(th.t(), c.dy.t()).t()
+    assert ((dw2.double() - ref).abs() <= tol + rnd(c.dt, ref.abs() + tol)).all()
+
+
 @pytest.mark.parametrize("keep", ["fp8", "full"])
 @pytest.mark.parametrize("t", list(DT))
 @pytest.mark.parametrize("T,d,I", SIZES)
@@ -156,21 +178,32 @@ def test_backward(T, d, I, t, keep):
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
     moe.moe_ffn_backward(c.dy, c.x, c.w13, c.w2, ac, s, dac, h, dx, dw13, dw2, dev_status=st)
     assert int(st) == 0
-    DAC, td, H, th = backward_ref(c, A, C)
-    assert ((dac.double() - DAC).abs() <= td).all()
-    assert ((h.double() - H).abs() <= th).all()
-    for got, (a, ta), b in ((dx, (DAC, td), c.w13.t()), (dw13, (DAC.t(), td.t()), c.x.t())):
-        ref, e = prod(a, b)
-        tol = e + spread(ta, b)
-        assert ((got.double() - ref).abs() <= tol + rnd(c.dt, ref.abs() + tol)).all()
-    ref, e = prod(c.dy.t(), H.t())
-    tol = e + spread(th.t(), c.dy.t()).t()
-    assert ((dw2.double() - ref).abs() <= tol + rnd(c.dt, ref.abs() + tol)).all()
+    check_backward(c, A, C, dac, h, dx, dw13, dw2)
     # one gradient at a time gives the same bits
     for k in range(3):
         out = [torch.empty_like(v) if i == k else None for i, v in enumerate((dx, dw13, dw2))]
         moe.moe_ffn_backward(c.dy, c.x, c.w13, c.w2, ac, s, dac, h, *out)
         assert torch.equal(out[k], (dx, dw13, dw2)[k])
+
+
+# few tokens with a long K: one to eight parts of K, one and two tiles of
+# tokens, features that leave the last 64 or more of a tile of 128 empty
+FEW = [(1, 6800, 408), (6, 392, 1536), (40, 4096, 136), (48, 1032, 328), (100, 264, 2048), (200, 2048, 192),
+       (300, 4104, 136)]
+
+
+@pytest.mark.parametrize("keep", ["fp8", "full"])
+@pytest.mark.parametrize("t", list(DT))
+@pytest.mark.parametrize("T,d,I", FEW)
+def test_few_tokens_kept(T, d, I, t, keep):
+    test_forward(T, d, I, t, keep)
+
+
+@pytest.mark.parametrize("keep", ["fp8", "full"])
+@pytest.mark.parametrize("t", list(DT))
+@pytest.mark.parametrize("T,d,I", FEW)
+def test_few_tokens_backward(T, d, I, t, keep):
+    test_backward(T, d, I, t, keep)
 
 
 def test_many_tiles_per_pair():
@@ -319,23 +352,22 @@ def test_side_streams_at_once_and_captured(T):
 
 
 def test_offsets_past_32_bits():
-    """Tokens whose elements lie beyond 2^31 give what the same tokens give in
-    a call that takes the same tiles."""
+    """Tokens whose elements lie beyond 2^31, against the formulas."""
     import fp8_block_scaled_affinity_b200 as moe
     need_gpu()
-    d, I = 4096, 64
+    d, I, dt = 4096, 64, torch.bfloat16
     T = 2 ** 31 // d + 4096
-    w13, w2 = rand(2 * I, d, seed=2, scale=d ** -0.5, dt=torch.bfloat16), rand(d, I, seed=3, dt=torch.bfloat16)
-    x = torch.zeros(T, d, dtype=torch.bfloat16, device=DEV)
-    x[-4096:] = rand(4096, d, seed=1, dt=torch.bfloat16)
-
-    def step(x):
-        n = x.shape[0]
-        e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
-        h, y, dac, h2, dx = e(n, I), e(n, d), e(n, 2 * I), e(n, I), e(n, d)
-        ac, s = torch.empty(n, 256, dtype=torch.uint8, device=DEV), torch.empty(2, n, device=DEV)
-        moe.moe_ffn_forward(x, w13, w2, h, y, ac, s)
-        moe.moe_ffn_backward(x, x, w13, w2, ac, s, dac, h2, dx)
-        return [v[-4096:] for v in (h, y, ac, s.t(), dac, h2, dx)]
-    for a, b in zip(step(x), step(x[-4096:].clone())):
-        assert torch.equal(a, b)
+    c = Case(0, d, I, dt)
+    c.w13, c.w2 = rand(2 * I, d, seed=2, scale=d ** -0.5, dt=dt), rand(d, I, seed=3, dt=dt)
+    x = torch.zeros(T, d, dtype=dt, device=DEV)
+    x[-4096:] = rand(4096, d, seed=1, dt=dt)
+    e = lambda *s: torch.empty(*s, dtype=dt, device=DEV)  # noqa: E731
+    h, y, dac, h2, dx = e(T, I), e(T, d), e(T, 2 * I), e(T, I), e(T, d)
+    ac, s = torch.empty(T, 256, dtype=torch.uint8, device=DEV), torch.empty(2, T, device=DEV)
+    moe.moe_ffn_forward(x, c.w13, c.w2, h, y, ac, s)
+    moe.moe_ffn_backward(x, x, c.w13, c.w2, ac, s, dac, h2, dx)
+    n = 600
+    c.x = c.dy = x[-n:]
+    check_forward(c, h[-n:], y[-n:], ac[-n:], s[:, -n:], "fp8")
+    kept = unpack64(ac[-n:], s[:, -n:])
+    check_backward(c, kept[:, :I], kept[:, 128:128 + I], dac[-n:], h2[-n:], dx[-n:], None, None)
