@@ -1130,8 +1130,10 @@ struct Maker {
 
 // The columns of a launch's pair tiles, and about how long it takes, in SM
 // clocks.  A stage of 64 K elements takes the MMA 2 clocks a column, and 100
-// more; a column of the epilogue costs `epilogue` clocks, under the next
-// tile's products but for the last tile's; starting and ending take 5500; and
+// more; a column of the epilogue costs `epilogue` clocks after the last tile,
+// and under the next tile's products no tile of kPlain takes less than 1200 and
+// 11 a column (the weight gradients of 16 tokens of d = 7168, inter = 2048: 24 us
+// in columns of 256, 29 of 128, 40 of 64); starting and ending take 5500; and
 // no launch ends before its longest tile.  So
 // few tiles are cut narrow (256 tokens, d = 512, inter = 256: dy W2 14 us in one
 // tile of 256 columns, 9 us in four of 64), and many take the width whose
@@ -1148,6 +1150,7 @@ struct Extent {
     int nkb;
 };
 constexpr int64_t kLaunchClocks = 5500;
+constexpr int kPlainClocks = 8, kGatedClocks = 16, kBackwardClocks = 66;
 PairPlan pair_plan(const Extent* e, int count, int epilogue, std::initializer_list<int> widths) {
     const int pairs = std::max(1, sm_count() / 2);
     PairPlan best;
@@ -1161,11 +1164,11 @@ PairPlan pair_plan(const Extent* e, int count, int epilogue, std::initializer_li
         }
         if (tiles == 0) return PairPlan{256, 0};
         main /= tiles;  // of an average tile
-        const int64_t epi = int64_t(epilogue) * nt;
+        const int64_t last = int64_t(epilogue) * nt;
+        const int64_t least = epilogue == kPlainClocks ? 1200 + 11 * nt : last;
+        const int64_t more = (tiles + pairs - 1) / pairs - 1;  // rounds over the pairs after the first
         const int64_t clocks =
-            kLaunchClocks +
-            std::max(longest, (tiles + pairs - 1) / pairs * std::max(main, epi)) +
-            std::min(main, epi);
+            kLaunchClocks + std::max(longest, main + more * std::max(main, least)) + last;
         if (clocks < best.clocks) {
             best.nt = nt;
             best.clocks = clocks;
@@ -1173,7 +1176,6 @@ PairPlan pair_plan(const Extent* e, int count, int epilogue, std::initializer_li
     }
     return best;
 }
-constexpr int kPlainClocks = 8, kGatedClocks = 16, kBackwardClocks = 66;
 
 // out [m, n] = A B^T over k: A is [m, k] in memory, or [k, m] (a_mn); B is
 // [n, k], or [k, n] (b_mn).
