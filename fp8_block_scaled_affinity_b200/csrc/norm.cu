@@ -17,9 +17,10 @@
 // registers leave room for one wide row at a time on an SM, whose loads and
 // barrier nothing else hides.  So rows are streamed: several ahead are copied
 // into shared memory in bulk, which goes on whatever the threads wait for
-// (4096 rows of 7168 kept in 8 bits: 47 us, 20 us more with each row loaded when
-// its turn comes).  Rows that are no multiple of 16 bytes are copied from
-// the 16-byte boundary before them, and read an element at a time.
+// (4096 rows of 7168 kept in 8 bits: 53 us, against 73 us with each row loaded
+// when its turn comes; 47 us since the partial sums leave 16 bytes a lane).
+// Rows that are no multiple of 16 bytes are copied from the 16-byte boundary
+// before them, and read an element at a time.
 #include <algorithm>
 
 #include "elem.cuh"
@@ -336,7 +337,8 @@ struct Turn {
 // 16 columns a thread in chunks of E: chunk j starts at column (t + j tpr) E.
 // Bound by the instructions of a row and the walk from one barrier to the next,
 // not by memory: 47 us for 4096 rows of 7168 kept in 8 bits, which read and
-// write 150 MB (23 us); 7 us more with 8 columns and twice the threads.
+// write 150 MB (23 us).  With 8 columns and twice the threads 60 us, where this
+// form took 53 us (its partial sums were stored 4 bytes a lane then: 6 us).
 template <class T, class X, int E>
 __global__ void __launch_bounds__(kStreamThreads)
     layernorm_backward_stream(const Rows dy, const Rows x, const float* __restrict__ x_scales,
