@@ -1217,11 +1217,11 @@ struct FewPlan {
     int tiles_t, tiles_w, nt, split, ring;
     int64_t clocks;
 };
-FewPlan few_plan(int mode, int64_t T, int rows, int nkb) {
+FewPlan few_tiles(int mode, int64_t T, int tiles_t, int rows, int nkb) {
     const int rows_per_tile = few_gated(mode) ? 64 : 128;
     const int max_split = mode == kFewKept ? kFewMaxSplit / 2 : kFewMaxSplit;
     FewPlan p;
-    p.tiles_t = int((T + kFewMaxTokens - 1) / kFewMaxTokens);
+    p.tiles_t = tiles_t;
     p.nt = int(((T + p.tiles_t - 1) / p.tiles_t + 15) / 16 * 16);
     p.tiles_w = (rows + rows_per_tile - 1) / rows_per_tile;
     if (mode == kFewKept) p.tiles_w += p.tiles_w & 1;
@@ -1242,6 +1242,17 @@ FewPlan few_plan(int mode, int64_t T, int rows, int nkb) {
     p.clocks =
         waves * ((nkb + p.split - 1) / p.split * int64_t(std::max(3 * p.nt, 128)) + 7000 + 30 * p.nt);
     return p;
+}
+// As few tiles of tokens as there can be, or two, four or eight times as many,
+// whose sums are sooner added up.
+FewPlan few_plan(int mode, int64_t T, int rows, int nkb) {
+    const int least = int((T + kFewMaxTokens - 1) / kFewMaxTokens);
+    FewPlan best = few_tiles(mode, T, least, rows, nkb);
+    for (int k = 2; k <= 8 && T >= 32 * int64_t(k) * least; k *= 2) {
+        const FewPlan p = few_tiles(mode, T, k * least, rows, nkb);
+        if (p.clocks < best.clocks) best = p;
+    }
+    return best;
 }
 // Whether a plan beats pairs: only where tiles of 256 x 256 leave pairs idle,
 // and then by the two estimates.  (Forward that keeps a and c, and backward: 48
