@@ -1231,16 +1231,29 @@ FewPlan few_tiles(int mode, int64_t T, int tiles_t, int rows, int nkb) {
     // other adds up, and the next product's start under this one: K is split
     // until there are more CTAs than SMs (one token of d = 7168, inter = 2048:
     // 22.9 us against 28.7 us with one CTA an SM).  Wider stages leave room
-    // for one: split until three quarters of the SMs have a CTA.
+    // for one: split until three quarters of the SMs have a CTA, and into
+    // clusters of eight only up to there (500 tokens, dy W2 of d = 2048, inter =
+    // 512: 16 such clusters do not find room at once and take 14.9 us, 32 with
+    // half an SM a CTA 9.6).
     const bool two = p.nt <= kFewShared;
     p.ring = two ? kFewRing2 : kFewRing1;
     p.split = 1;
+    const int pair = mode == kFewKept ? 2 : 1;
+    auto room = [&](int split) {
+        return two || pair * split < 8 || tiles * split * 4 <= 3 * int64_t(sms);
+    };
     while (p.split < max_split && tiles * p.split * 4 < int64_t(sms) * (two ? 4 : 3) &&
-           nkb >= 8 * p.split)
+           nkb >= 8 * p.split && room(2 * p.split))
         p.split *= 2;
-    const int64_t waves = (tiles * p.split + sms - 1) / sms;
-    p.clocks =
-        waves * ((nkb + p.split - 1) / p.split * int64_t(std::max(3 * p.nt, 128)) + 7000 + 30 * p.nt);
+    // Two on an SM take turns at its operands, and only a quarter longer before
+    // and after them (64 tokens, d = 7168, inter = 2048 forward: 25.9 us, h W2^T
+    // in pairs 28.3; 256 tokens, d = 4096, inter = 1024: 20.7 us in tiles of 64
+    // tokens, two an SM, and 19.4 in tiles of 128).
+    const int64_t ctas = tiles * p.split, at_once = int64_t(sms) * (two ? 2 : 1);
+    const int64_t k = (nkb + p.split - 1) / p.split * std::max(3 * p.nt, 128);
+    const int64_t rest = 7000 + 30 * p.nt;
+    p.clocks = (ctas + at_once - 1) / at_once *
+               (two && ctas > sms ? 2 * k + rest * 5 / 4 : k + rest);
     return p;
 }
 // As few tiles of tokens as there can be, or two, four or eight times as many,

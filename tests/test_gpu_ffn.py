@@ -189,7 +189,7 @@ def test_backward(T, d, I, t, keep):
 # few tokens with a long K: one to eight parts of K, one and two tiles of
 # tokens, features that leave the last 64 or more of a tile of 128 empty
 FEW = [(1, 6800, 408), (6, 392, 1536), (40, 4096, 136), (48, 1032, 328), (100, 264, 2048), (200, 2048, 192),
-       (300, 4104, 136)]
+       (300, 4104, 136), (500, 2048, 512), (64, 4096, 2048)]
 
 
 @pytest.mark.parametrize("keep", ["fp8", "full"])
