@@ -1365,6 +1365,15 @@ template <class T>
 int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t rows, int d, int I,
             void* h, void* y, void* ac, int kept, float* ac_scales, int* dev_status,
             cudaStream_t st) {
+    int rc;
+    // One token, or a few with few weights (a token's multiplications cost as
+    // much time as its weights' bytes: 2 and 4 tokens of 88 MB of weights take
+    // 25 and 36 us as vectors and 23 us as tiles, of 0.8 MB 3.4 and 9.3 us).
+    if (kept == kKeptNone && (rows == 1 || (rows <= kVecTokens &&
+                                            rows * 6 * int64_t(d) * I <= 100000000))) {
+        rc = launch_vec<true, T>(w13, x, h, int(rows), I, d, false, st);
+        return rc != MOE_OK ? rc : launch_vec<false, T>(w2, h, y, int(rows), d, I, true, st);
+    }
     const int kd = (d + kTileK - 1) / kTileK, ki = (I + kTileK - 1) / kTileK;
     // few tokens: whichever way takes fewer clocks.  (One token, d = 7168,
     // inter = 2048: 70 us in pairs of CTAs.)  a and c are kept in 8 bits from
@@ -1377,50 +1386,38 @@ int forward(Maker mk, const void* x, const void* w13, const void* w2, int64_t ro
     const FewPlan fb = few_plan(kFewPlain, rows, d, ki);
     const bool few_a = few_better(fa, rows, 2 * int64_t(I), pa);
     const bool few_b = few_better(fb, rows, d, pb);
-    int rc;
-    // One token, or a few with few weights (a token's multiplications cost as
-    // much time as its weights' bytes: 2 and 4 tokens of 88 MB of weights take
-    // 25 and 36 us as vectors and 23 us as tiles, of 0.8 MB 3.4 and 9.3 us).
-    if (kept == kKeptNone && (rows == 1 || (rows <= kVecTokens &&
-                                            rows * 6 * int64_t(d) * I <= 100000000))) {
-        rc = launch_vec<true, T>(w13, x, h, int(rows), I, d, false, st);
-        return rc != MOE_OK ? rc : launch_vec<false, T>(w2, h, y, int(rows), d, I, true, st);
-    }
     if (few_a) {
         rc = kept == kKeptNone
                  ? launch_few<kFewGated, T>(mk, fa, w13, x, h, rows, I, d, {}, dev_status, false, st)
                  : launch_few<kFewKept, T>(mk, fa, w13, x, h, rows, I, d, {ac, ac_scales, kept, nullptr},
                                            dev_status, false, st);
-        if (rc != MOE_OK) return rc;
-        if (few_b)
-            return launch_few<kFewPlain, T>(mk, fb, w2, h, y, rows, d, I, {}, dev_status, true, st);
-    }
-    Args a = make_args(rows, I, dev_status);
-    product(a, mk, x, false, w13, false, h, rows, 2 * int64_t(I), d, pa.nt);
-    // the gated tile: nt / 2 features of W1 and of W3
-    Problem& p = a.p[0];
-    p.n = I;
-    p.tiles_n = (I + pa.nt / 2 - 1) / (pa.nt / 2);
-    a.tiles = p.tiles_m * p.tiles_n;
-    mk.output(&p.out, h, rows, I, I);
-    a.ac = ac;
-    a.ac_scales = ac_scales;
-    if (kept == kKept16) {
-        mk.output(&a.o1, ac, rows, I, 2 * int64_t(I));
-        mk.output(&a.o2, static_cast<uint16_t*>(ac) + I, rows, I, 2 * int64_t(I));
-    }
-    Args b = make_args(rows, I, dev_status);
-    product(b, mk, h, false, w2, false, y, rows, d, I, pb.nt);
-    b.wait_first = 1;
-    if (!mk.ok) return MOE_ERR_CUDA;
-    if (!few_a) {
+    } else {
+        Args a = make_args(rows, I, dev_status);
+        product(a, mk, x, false, w13, false, h, rows, 2 * int64_t(I), d, pa.nt);
+        // the gated tile: nt / 2 features of W1 and of W3
+        Problem& p = a.p[0];
+        p.n = I;
+        p.tiles_n = (I + pa.nt / 2 - 1) / (pa.nt / 2);
+        a.tiles = p.tiles_m * p.tiles_n;
+        mk.output(&p.out, h, rows, I, I);
+        a.ac = ac;
+        a.ac_scales = ac_scales;
+        if (kept == kKept16) {
+            mk.output(&a.o1, ac, rows, I, 2 * int64_t(I));
+            mk.output(&a.o2, static_cast<uint16_t*>(ac) + I, rows, I, 2 * int64_t(I));
+        }
+        if (!mk.ok) return MOE_ERR_CUDA;
         rc = kept == kKept8    ? launch<kGated, kKept8, T>(a, st)
              : kept == kKept16 ? launch<kGated, kKept16, T>(a, st)
                                : launch<kGated, kKeptNone, T>(a, st);
-        if (rc != MOE_OK) return rc;
     }
-    return few_b ? launch_few<kFewPlain, T>(mk, fb, w2, h, y, rows, d, I, {}, dev_status, true, st)
-                 : launch<kPlain, kKeptNone, T>(b, st);
+    if (rc != MOE_OK) return rc;
+    // (laid out while the first product is on its way)
+    if (few_b) return launch_few<kFewPlain, T>(mk, fb, w2, h, y, rows, d, I, {}, dev_status, true, st);
+    Args b = make_args(rows, I, dev_status);
+    product(b, mk, h, false, w2, false, y, rows, d, I, pb.nt);
+    b.wait_first = 1;
+    return mk.ok ? launch<kPlain, kKeptNone, T>(b, st) : MOE_ERR_CUDA;
 }
 
 template <class T>
