@@ -1537,7 +1537,9 @@ extern "C" MOE_API int moe_ffn_backward(const void* dy, const void* x, const voi
     if (!device_is_sm100()) return MOE_ERR_DEVICE;
     return type == MOE_T_BF16
                ? backward<bf16_t>(maker(type), dy, x, w13, w2, const_cast<void*>(ac), kept,
-                                  const_cast<float*>(ac_scales), T, d, inter, dac, h, dx, dw13, dw2, dev_status, st)
+                                  const_cast<float*>(ac_scales), T, d, inter, dac, h, dx, dw13,
+                                  dw2, dev_status, st)
                : backward<f16_t>(maker(type), dy, x, w13, w2, const_cast<void*>(ac), kept,
-                                 const_cast<float*>(ac_scales), T, d, inter, dac, h, dx, dw13, dw2, dev_status, st);
+                                 const_cast<float*>(ac_scales), T, d, inter, dac, h, dx, dw13, dw2,
+                                 dev_status, st);
 }
