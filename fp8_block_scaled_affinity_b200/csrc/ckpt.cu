@@ -1,8 +1,8 @@
 // Activation checkpoints in 8 bits: a matrix kept between the forward and
 // the backward pass as E4M3 codes with one fp32 scale per 1x128 tile of a
-// row: scale = amax / 448, code = E4M3(v (448 / amax)), kept_scale's rule.  Codes lie in [rows, cols rounded up to 128] bytes, so a
-// tile is one 128-byte line; scales in [tiles, rows], the layout the grouped
-// GEMM reads.
+// row: scale = amax / 448, code = E4M3(v (448 / amax)), kept_scale's rule.
+// Codes lie in [rows, cols rounded up to 128] bytes, so a tile is one 128-byte
+// line; scales in [tiles, rows], the layout the grouped GEMM reads.
 //
 // All passes here are bound by memory: each value is read once, each code
 // written once.
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_ckpt_kernel(
     }
     // the divisions of all the warp's tiles at once, a tile a lane
     float scale, inv;
-    scale_from_amax(amax, scale, inv);
+    scale_from_amax(kept_amax(amax), scale, inv);
     if (lane < 2 * RW) sout[lane & 1][warp * RW + (lane >> 1)] = scale;
 #pragma unroll
     for (int r = 0; r < RW; ++r) {

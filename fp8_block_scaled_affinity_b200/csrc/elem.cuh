@@ -62,12 +62,20 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // fp32(448 fp32(1 / amax)), both 1 for a tile of zeros.  (The online
 // quantisers round 448 / amax once; here one reciprocal and one product are
 // enough, and a code differs only where its value lies within an fp32
-// rounding of the border between two codes.)
+// rounding of the border between two codes.)  448 / amax passes the fp32 range
+// below 1.32e-36, where zeros would become 0 * inf: such an amax counts as
+// 2^-119 (1.5e-36), whose inverse is exact and whose scale is subnormal with 22
+// bits, and the tile's values keep what E4M3 has down to 2^-10 of that scale.
+constexpr float kLeastAmax = 0x1p-119f;
+__device__ __forceinline__ float kept_amax(float amax) {
+    return amax == 0.0f ? 0.0f : fmaxf(amax, kLeastAmax);
+}
 __device__ __forceinline__ void kept_scale(float amax, float& scale, float& inv) {
     if (amax == 0.0f) {
         scale = 1.0f;
         inv = 1.0f;
     } else {
+        amax = fmaxf(amax, kLeastAmax);
         scale = __fdiv_rn(amax, 448.0f);
         inv = __fmul_rn(__frcp_rn(amax), 448.0f);
     }

@@ -787,9 +787,12 @@ MOE_API int moe_layernorm_backward(const void* dy, int type, const void* x, int 
  * scale per 1x128 tile of a row ("FP8 mixed precision training": activations
  * kept in FP8 for the backward pass): scale = fp32(amax / 448), code =
  * E4M3(fp32(v * inverse)) with inverse = fp32(448 * fp32(1 / amax)); a tile
- * of zeros has scale 1.  (The scale rule at the top of this file with the
- * inverse rounded twice: codes differ only next to a border.)  A tile that holds an infinity comes back as NaN; a NaN comes back
- * as NaN and leaves the other values of its tile alone.
+ * of zeros has scale 1, and an amax between 0 and 2^-119 (1.5e-36), next to
+ * which the inverse leaves the fp32 range, counts as 2^-119.  (The scale rule
+ * at the top of this file with the inverse rounded twice: codes differ only
+ * next to a border.)  Every finite tile comes back finite.  A tile that holds
+ * an infinity comes back as NaN; a NaN comes back as NaN and leaves the other
+ * values of its tile alone.
  *   q       uint8 [rows, moe_ckpt_row_bytes(cols)], 16-byte aligned; the
  *           bytes past the last column of a row are written as zeros
  *   scales  fp32 [ceil(cols / 128), rows]
@@ -809,7 +812,8 @@ MOE_API int moe_layernorm_backward(const void* dy, int type, const void* x, int 
  * The backward steps that read a checkpoint where it lies:
  * moe_swiglu_backward_quant_ckpt: moe_swiglu_backward_quant with [a | c] kept
  *   as ac_q (uint8 [rows, 2 inter]) and ac_scales (fp32 [2 inter / 128,
- *   rows_total]).
+ *   rows_total]); a tile of [da | dc] whose amax is between 0 and 2^-119 is
+ *   scaled as one of 2^-119.
  * moe_wgrad_quant_h_ckpt, moe_wgrad_quant_dac_ckpt: moe_wgrad_quant_h and
  *   _dac with [a | c] kept so; rows_total is the scales' row length.
  * moe_gate_backward_ckpt: moe_gate_backward with the expert outputs kept as
