@@ -88,13 +88,21 @@ class LayerNorm:
     GPU, or None) and what its backward pass needs of the last forward_train.
 
     forward_train(x, keep): keep="full" keeps x itself (it must stay unchanged
-    until backward() has run, so y may not be x), "fp8" an 8-bit copy of it.  backward(dy) leaves
-    the parameters' gradients in dweight and dbias (fp32)."""
+    until backward() has run, so y may not be x), "fp8" an 8-bit copy of it.
+    backward(dy) leaves the parameters' gradients in dweight and dbias (fp32).
+    A wait of the backward pass that ran out shows in status(), or in the status
+    word of the layer whose norm this is."""
 
     def __init__(self, weight=None, bias=None, eps: float = 1e-5):
         self.weight, self.bias, self.eps = weight, bias, float(eps)
         self.dweight = self.dbias = None
+        self.dev_status = None if weight is None else self._status_word(weight.device)
         self._kept = None
+
+    @staticmethod
+    def _status_word(device):
+        import torch
+        return torch.zeros((1,), dtype=torch.int32, device=device)
 
     @_on_stream
     def forward(self, x, y=None, stream=None):
@@ -121,11 +129,17 @@ class LayerNorm:
         return y
 
     @_on_stream
-    def backward(self, dy, stream=None):
-        """dx (dy's type) of the last forward_train(); dy of x's type or fp32."""
+    def backward(self, dy, stream=None, dev_status=None):
+        """dx (dy's type) of the last forward_train(); dy of x's type or fp32.
+        dev_status: the word that a wait which ran out is reported on (None: the
+        norm's own)."""
         import torch
         if self._kept is None:
             raise RuntimeError("backward() needs a forward_train() first")
+        if dev_status is None:
+            if self.dev_status is None:
+                self.dev_status = self._status_word(dy.device)
+            dev_status = self.dev_status
         x, scales, mean, rstd = self._kept
         rows, cols = dy.shape
         dx = torch.empty_like(dy)
@@ -134,8 +148,12 @@ class LayerNorm:
         ws = torch.empty((max(16, moe_layernorm_backward_workspace_size(rows, cols)),),
                          dtype=torch.uint8, device=dy.device)
         moe_layernorm_backward(dy, x, scales, self.weight, mean, rstd, dx, self.dweight,
-                               self.dbias, ws, stream=stream)
+                               self.dbias, ws, dev_status, stream)
         return dx
+
+    def status(self, stream=None) -> int:
+        """Device status word (0 = fine); synchronises the stream."""
+        return 0 if self.dev_status is None else moe_read_status(self.dev_status, stream)
 
 
 class GatedFfn:
@@ -209,7 +227,7 @@ class GatedFfn:
         moe_ffn_backward(dy, n, self.w13, self.w2, ac, scales, self._hidden(dy, 2 * inter),
                          self._hidden(dy, inter), dx, dw13, dw2, self.dev_status, stream)
         if self.norm is not None:
-            dx = self.norm.backward(dx, stream=stream)
+            dx = self.norm.backward(dx, stream=stream, dev_status=self.dev_status)
         return (dx, dw13, dw2) if wgrad else dx
 
     def status(self, stream=None) -> int:
@@ -510,7 +528,7 @@ class MoeLayer:
         mark("dx_combine")
         self.last_dgate, self.last_du = dgate, du
         if self.norm is not None:
-            dx = self.norm.backward(dx, stream=stream)
+            dx = self.norm.backward(dx, stream=stream, dev_status=self.dev_status)
             mark("norm_backward")
         if not wgrad:
             return dx, d_router_w

@@ -771,7 +771,8 @@ MOE_API int moe_grouped_gemm_wgrad(int n_groups, const int32_t* kb_offsets, int 
  *                bytes, 16-byte aligned; not read when dweight and dbias are
  *                both NULL.  Calls in flight together need their own.
  * Errors: MOE_ERR_ARG (types, eps < 0), MOE_ERR_SHAPE, MOE_ERR_NULL,
- * MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE, MOE_ERR_CUDA. */
+ * MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE, MOE_ERR_CUDA; the backward
+ * pass MOE_DEV_TIMEOUT on dev_status, with dx and both sums then unfinished. */
 MOE_API int moe_layernorm_forward(const void* x, int type, int64_t rows, int cols,
                                   const float* weight, const float* bias, float eps, void* y,
                                   float* mean, float* rstd, int* dev_status, void* stream);
