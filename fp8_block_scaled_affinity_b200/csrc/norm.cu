@@ -517,10 +517,18 @@ __global__ void __launch_bounds__(kStreamThreads)
     }
 }
 
+// A value that the kernel before this one writes: a plain load that the
+// compiler leaves behind the wait, where one through a const __restrict__
+// pointer counts as read-only for the whole kernel.
+__device__ __forceinline__ float load_written(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // Column sums of the partial rows [n][2 cols]: a CTA per 32 columns, its 32
 // warps take every 32nd row, then their sums are added in order.
-__global__ void __launch_bounds__(1024) layernorm_sum_kernel(const float* __restrict__ part, int n,
-                                                             int cols,
+__global__ void __launch_bounds__(1024) layernorm_sum_kernel(const float* part, int n, int cols,
                                                              float* __restrict__ dweight,
                                                              float* __restrict__ dbias) {
     __shared__ float s[32][33];
@@ -531,7 +539,7 @@ __global__ void __launch_bounds__(1024) layernorm_sum_kernel(const float* __rest
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c < 2 * cols)
 #pragma unroll 8
-        for (int i = warp; i < n; i += 32) a += part[int64_t(i) * 2 * cols + c];
+        for (int i = warp; i < n; i += 32) a += load_written(part + int64_t(i) * 2 * cols + c);
     s[warp][lane] = a;
     __syncthreads();
     // warp w adds up column w of the 32: lanes are the warps' sums
