@@ -2019,48 +2019,55 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// 2D uint8 map over [rows, cols] (cols contiguous), box = [box_rows, 128].
-bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+// Encodes a map.  The call needs a current context, which a host thread that
+// has not used the runtime yet lacks; cudaSetDevice makes its device's context
+// current there.
+template <class... Args>
+bool encode(Args... args) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
+    if (fn(args...) == CUDA_SUCCESS) return true;
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess &&
+           fn(args...) == CUDA_SUCCESS;
+}
+
+// 2D uint8 map over [rows, cols] (cols contiguous), box = [box_rows, 128].
+bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
     cuuint64_t dims[2] = {cols, rows};
     cuuint64_t strides[1] = {cols};
     cuuint32_t box[2] = {128, box_rows};
     cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // 2D output map over [rows, cols] of fp32 or bf16 (cols contiguous): box = 32 rows x
 // 128 bytes, 128-byte swizzle (the layout of the epilogue's parking tiles).
 bool make_out_map(CUtensorMap* m, void* base, uint64_t rows, uint64_t cols, bool bf16) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
     const uint32_t esize = bf16 ? 2 : 4;
     cuuint64_t dims[2] = {cols, rows};
     cuuint64_t strides[1] = {cols * esize};
     cuuint32_t box[2] = {128 / esize, 32};
     cuuint32_t estr[2] = {1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base,
-              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                  base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // 2D map over [rows, cols] of any element type, rows pitch_bytes apart.
 bool make_map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t rows,
                  uint64_t cols, uint64_t pitch_bytes, uint32_t box_rows,
                  uint32_t box_cols, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promote) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
     cuuint64_t dims[2] = {cols, rows};
     cuuint64_t strides[1] = {pitch_bytes};
     cuuint32_t box[2] = {box_cols, box_rows};
     cuuint32_t estr[2] = {1, 1};
-    return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promote,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promote,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool device_is_sm100() {
