@@ -20,6 +20,13 @@ inline int check_launch() {
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// A runtime call that failed: its error is taken back, so that the thread's
+// next check_launch() does not find it.
+inline int cuda_failed() {
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+}
+
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }

@@ -1077,10 +1077,8 @@ int pair_units(cudaLaunchConfig_t& cfg) {
     if (cache[dev] == 0) {
         int n = 0;
         cfg.gridDim = dim3(unsigned(2 * (sm_count() / 2)), 1, 1);
-        if (cudaOccupancyMaxActiveClusters(&n, ffn_kernel<EPI, KEPT, T>, &cfg) != cudaSuccess) {
-            (void)cudaGetLastError();
+        if (cudaOccupancyMaxActiveClusters(&n, ffn_kernel<EPI, KEPT, T>, &cfg) != cudaSuccess)
             return 0;
-        }
         cache[dev] = std::min(n, sm_count() / 2);
     }
     return cache[dev];
@@ -1102,10 +1100,10 @@ int launch(Args& a, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const int units = pair_units<EPI, KEPT, T>(cfg);
-    if (units < 1) return MOE_ERR_CUDA;
+    if (units < 1) return cuda_failed();
     if (a.wait_first) cfg.numAttrs = 2;
     cfg.gridDim = dim3(unsigned(2 * std::min(units, a.tiles)), 1, 1);
-    if (cudaLaunchKernelEx(&cfg, ffn_kernel<EPI, KEPT, T>, a) != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, ffn_kernel<EPI, KEPT, T>, a) != cudaSuccess) return cuda_failed();
     return check_launch();
 }
 
@@ -1296,7 +1294,7 @@ int launch_vec_tok(const void* w, const void* x, void* out, int tokens, int rows
     if (cudaLaunchKernelEx(&cfg, vec_kernel<GATED, TOK, T>, static_cast<const T*>(w),
                            static_cast<const T*>(x), static_cast<T*>(out), tokens, rows, K, parts,
                            int(after)) != cudaSuccess)
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     return check_launch();
 }
 template <bool GATED, class T>
@@ -1339,9 +1337,11 @@ int launch_few(Maker& mk, const FewPlan& p, const void* w, const void* x, void* 
     a.wait_first = after;
     a.dev_status = dev_status;
     a.wait_limit_ns = wait_limit_ns();
+    // (leave for either ring, whichever this call takes: the limit is the
+    // device's, and another thread may be between its own and its launch)
     if (cudaFuncSetAttribute(few_kernel<MODE, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(few_smem(p.ring))) != cudaSuccess)
-        return MOE_ERR_CUDA;
+                             int(few_smem(kFewRing1))) != cudaSuccess)
+        return cuda_failed();
     const int pair = MODE == kFewKept ? 2 : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(pair * p.split), unsigned(p.tiles_w / pair), unsigned(p.tiles_t));
@@ -1357,7 +1357,7 @@ int launch_few(Maker& mk, const FewPlan& p, const void* w, const void* x, void* 
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = after ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, few_kernel<MODE, T>, a) != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, few_kernel<MODE, T>, a) != cudaSuccess) return cuda_failed();
     return check_launch();
 }
 
@@ -1525,7 +1525,7 @@ extern "C" MOE_API int moe_ffn_backward(const void* dy, const void* x, const voi
         const size_t n = size_t(d) * size_t(inter) * 2;
         if ((dw13 && cudaMemsetAsync(dw13, 0, 2 * n, st) != cudaSuccess) ||
             (dw2 && cudaMemsetAsync(dw2, 0, n, st) != cudaSuccess))
-            return MOE_ERR_CUDA;
+            return cuda_failed();
         return MOE_OK;
     }
     if (!dy || !w2 || !ac || !dac || !h || (dx && !w13) || (dw13 && !x)) return MOE_ERR_NULL;

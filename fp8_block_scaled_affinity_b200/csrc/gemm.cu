@@ -1635,7 +1635,7 @@ int launch(const GemmParams& p, const CUtensorMap& mw, const AMaps& ma, const CU
     if (cudaFuncSetAttribute(grouped_gemm_kernel<PAIR, SWIGLU, WIDE, KEEP>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(smem_bytes<PAIR, SWIGLU, WIDE>())) != cudaSuccess)
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     if (!PAIR) {
         grouped_gemm_kernel<PAIR, SWIGLU, WIDE, KEEP>
             <<<sm_count(), kThreads, smem_bytes<PAIR, SWIGLU, WIDE>(), st>>>(mw, ma, mo, p);
@@ -1655,7 +1655,7 @@ int launch(const GemmParams& p, const CUtensorMap& mw, const AMaps& ma, const CU
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<PAIR, SWIGLU, WIDE, KEEP>, mw, ma, mo, p) !=
         cudaSuccess)
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     return check_launch();
 }
 

@@ -577,9 +577,12 @@ int slot_bytes(int64_t row) { return int((row + 15) / 16 * 16 + kSlotPad); }
 Rows make_rows(const void* p, int64_t rows, int64_t pitch, int64_t bytes) {
     return Rows{static_cast<const char*>(p), pitch, rows * pitch / 16 * 16, int(bytes)};
 }
+// Leave for a launch of any size, never for this call's alone: the limit is the
+// device's, and another thread may be between its own and its launch.
+constexpr int kStreamSmem = std::max(kSmBytes, 2 * (2 * kPerThread * kStreamThreads * 4 + 2 * kSlotPad));
 template <class K>
-bool allow_smem(K kernel, int bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+bool allow_smem(K kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem) ==
            cudaSuccess;
 }
 int round_threads(int chunks, int ch) { return ((chunks + ch - 1) / ch + 31) / 32 * 32; }
@@ -637,7 +640,7 @@ int backward_launch(const BwdArgs& a, int threads, cudaStream_t st) {
 template <class T, class X, int E>
 int backward_stream(const BwdArgs& a, int x_slot, const Stream& s, cudaStream_t st) {
     const int bytes = s.slot * s.ahead;
-    if (!allow_smem(layernorm_backward_stream<T, X, E>, bytes)) return MOE_ERR_CUDA;
+    if (!allow_smem(layernorm_backward_stream<T, X, E>)) return cuda_failed();
     const int64_t row = int64_t(a.cols) * int64_t(sizeof(T));
     layernorm_backward_stream<T, X, E>
         <<<backward_ctas(a.rows, a.cols), stream_threads(a.cols), bytes, st>>>(
@@ -734,7 +737,7 @@ extern "C" MOE_API int moe_layernorm_backward(const void* dy, int type, const vo
         // no rows: the parameters' gradients are empty sums
         for (float* g : {dweight, dbias})
             if (g && cudaMemsetAsync(g, 0, sizeof(float) * size_t(cols), st) != cudaSuccess)
-                return MOE_ERR_CUDA;
+                return cuda_failed();
         return MOE_OK;
     }
     if (!dy || !x || !mean || !rstd || !dx) return MOE_ERR_NULL;
@@ -768,6 +771,6 @@ extern "C" MOE_API int moe_layernorm_backward(const void* dy, int type, const vo
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, layernorm_sum_kernel, static_cast<const float*>(a.part),
                            backward_ctas(rows, cols), cols, dweight, dbias) != cudaSuccess)
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     return check_launch();
 }
