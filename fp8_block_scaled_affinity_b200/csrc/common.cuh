@@ -106,11 +106,13 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 uint64_t wait_limit_ns();
 
 // Host-driven fault injection (MOEFP8_FAULT in the environment, read at
-// every call): kFaultGemmProducer makes the single-CTA grouped GEMM's TMA
-// producer withhold the loads of its first stage, so that the MMA issuer's
-// bounded wait on that stage runs out (MOE_DEV_TIMEOUT) and the kernel
-// unwinds.  Nothing faults, traps or hangs: the wait limit ends it.
-enum FaultKind { kFaultNone = 0, kFaultGemmProducer = 1 };
+// every call): a kernel's TMA producer withholds the loads of its first stage,
+// so that the bounded wait on that stage runs out (MOE_DEV_TIMEOUT) and the
+// kernel unwinds.  Nothing faults, traps or hangs: the wait limit ends it.
+//   kFaultGemmProducer  the single-CTA grouped GEMM
+//   kFaultFfnProducer   the dense block's kernels that load by TMA
+//   kFaultNormRows      the norm's backward pass that streams rows
+enum FaultKind { kFaultNone = 0, kFaultGemmProducer = 1, kFaultFfnProducer = 2, kFaultNormRows = 3 };
 int fault_injection();
 
 }  // namespace moe

@@ -95,6 +95,7 @@ struct Args {
     int wait_first;          // 1: operands come from the kernel before this one
     int* dev_status;
     uint64_t wait_limit_ns;
+    int fault;               // FaultKind
 };
 
 struct Shared {
@@ -105,6 +106,7 @@ struct Shared {
     uint64_t drain;
     PairState ps;
     uint32_t tmem_base;
+    uint32_t issued[4];      // the leader's: steps that each of the pair's producers has loaded
 };
 
 template <int EPI>
@@ -151,7 +153,7 @@ __device__ __forceinline__ void producer(const Args& a, uint8_t* smem, Shared* s
     const bool lead = elect_one();
     // the leader's barrier of stage 0
     const uint32_t bar0 = uniform(mapa(smem_u32(&ss->full[0]), 0));
-    uint32_t s = 0, par = 1, issued = 0, issued_parity = 0;
+    uint32_t s = 0, par = 1, issued = 0;
     bool ok = true;
     for (int t = unit; ok && t < a.tiles; t += units) {
         const Tile w = decode_for<EPI>(a, t);
@@ -175,7 +177,9 @@ __device__ __forceinline__ void producer(const Args& a, uint8_t* smem, Shared* s
                 smem_u32(smem) + s * uint32_t(kStageBytes) + (IS_A ? 0u : uint32_t(kOperandBytes));
             const uint32_t bar = bar0 + 8 * s;
             const int k0 = kb * kTileK;
-            if (lead) {
+            const bool withheld =
+                IS_A && rank == 0 && a.fault == kFaultFfnProducer && issued == 0;
+            if (lead && !withheld) {
                 if (IS_A && rank == 0) mbar_arrive_expect_tx(smem_u32(&ss->full[s]), tx);
                 if (mn) {
                     pair_tma_load_2d(dst, map, bar, first, k0);
@@ -184,19 +188,14 @@ __device__ __forceinline__ void producer(const Args& a, uint8_t* smem, Shared* s
                     pair_tma_load_2d(dst, map, bar, k0, first);
                 }
             }
-            issued |= 1u << s;
-            issued_parity = (issued_parity & ~(1u << s)) | ((par ^ 1u) << s);
+            ++issued;
             if (++s == kStages) {
                 s = 0;
                 par ^= 1u;
             }
         }
     }
-    if (!ok && rank == 0 && IS_A && lead)  // loads in flight land before the CTA leaves
-        for (int i = 0; i < kStages; ++i)
-            if ((issued >> i) & 1u)
-                mbar_quiesce(smem_u32(&ss->full[i]), (issued_parity >> i) & 1u, nullptr,
-                             quiesce_ns(ss->ps.wait_limit));
+    if (lead) st_cluster(mapa(smem_u32(&ss->issued[2 * rank + (IS_A ? 0 : 1)]), 0), issued);
     __syncwarp();
 }
 
@@ -550,6 +549,18 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
     // neither CTA leaves while the other may still signal its barriers or
     // the leader's MMAs may still read its shared memory
     cluster_sync();
+    // Given up (both CTAs' flags are raised together, and by nobody any more):
+    // loads of either CTA may be in flight, whichever wait ran out.  The
+    // barriers they arrive on are the leader's.
+    if (*reinterpret_cast<volatile int*>(&ss->ps.abort_flag)) {
+        if (rank == 0 && threadIdx.x == 0) {
+            const volatile uint32_t* n = ss->issued;
+            ring_quiesce(ss->full, kStages, max(max(n[0], n[1]), max(n[2], n[3])),
+                         ss->ps.wait_limit);
+        }
+        __syncwarp();
+        cluster_sync();
+    }
     if (warp == 1) {
         fence_after();
         pair_tmem_free(tmem_base);
@@ -599,6 +610,7 @@ struct FewArgs {
     int wait_first; // 1: x comes from the kernel before this one
     int* dev_status;
     uint64_t wait_limit_ns;
+    int fault;      // FaultKind
 };
 
 struct FewShared {
@@ -840,10 +852,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     const uint32_t tmem = uniform(ss->tmem_base);
     const int stage_bytes = kOperandBytes + a.nt * 128;
     bool ok = true;
+    int loaded = 0;  // steps that warp 0 has loaded
     if (warp == 0) {
         const bool lead = elect_one();
         const int w0 = wt * (GATED ? 64 : 128);
         auto load_w = [&](int i, int s) {
+            if (i == 0 && a.fault == kFaultFfnProducer) return;
             const int k0 = (kb0 + i) * kTileK;
             const uint32_t bar = smem_u32(&ss->full[s]);
             const uint32_t dst = smem_u32(smem) + s * stage_bytes;
@@ -857,6 +871,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             }
         };
         auto load_x = [&](int i, int s) {
+            if (i == 0 && a.fault == kFaultFfnProducer) return;
             tma_load_2d(smem_u32(smem) + s * stage_bytes + kOperandBytes, &a.x,
                         smem_u32(&ss->full[s]), (kb0 + i) * kTileK, int(t0));
         };
@@ -885,12 +900,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 par ^= 1u;
             }
         }
-        if (!ok && lead)  // loads in flight land before the CTA leaves
-            for (int j = max(0, i - a.stages); j < i; ++j)
-                mbar_quiesce(smem_u32(&ss->full[j % a.stages]), (j / a.stages) & 1u, nullptr,
-                             quiesce_ns(a.wait_limit_ns));
+        loaded = i;
     } else if (warp == 1) {
         const bool lead = elect_one();
+        // (the limit of its waits does not run while the kernel before this one does)
+        if (a.wait_first) wait_dependencies();
         const uint32_t idesc = idesc_f16(std::is_same<T, bf16_t>::value, MN, 0, 128, a.nt);
         constexpr uint32_t w_step = MN ? 2048 / 16 : 32 / 16;  // as in the pairs' issuer
         const uint64_t desc0 = sw128_desc16(smem_u32(smem), kPieceBytes);
@@ -925,8 +939,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     // the products are done (warp 1 has waited for them), or given up
     const bool bad = __syncthreads_or(!ok || *reinterpret_cast<volatile int*>(&ss->abort_flag));
     fence_after();
+    // given up, whoever's wait ran out: loads may be in flight into the stages,
+    // over which no sums are laid then
+    if (bad && warp == 0) {
+        if (lane == 0)
+            ring_quiesce(ss->full, uint32_t(a.stages), uint32_t(loaded), a.wait_limit_ns);
+        __syncwarp();
+    }
     float* part = reinterpret_cast<float*>(smem);  // [nt][128]
-    if (warp >= 2) {
+    if (warp >= 2 && !bad) {
         const int q = warp & 3;  // the quarter of the lanes it may read
         for (int c = warp < 6 ? 0 : 16; c < a.nt; c += 32) {
             uint32_t v[16];
@@ -1203,6 +1224,7 @@ Args make_args(int64_t T, int inter, int* dev_status) {
     a.inter = inter;
     a.dev_status = dev_status;
     a.wait_limit_ns = wait_limit_ns();
+    a.fault = fault_injection();
     return a;
 }
 
@@ -1337,6 +1359,7 @@ int launch_few(Maker& mk, const FewPlan& p, const void* w, const void* x, void* 
     a.wait_first = after;
     a.dev_status = dev_status;
     a.wait_limit_ns = wait_limit_ns();
+    a.fault = fault_injection();
     // (leave for either ring, whichever this call takes: the limit is the
     // device's, and another thread may be between its own and its launch)
     if (cudaFuncSetAttribute(few_kernel<MODE, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -48,6 +48,8 @@ uint64_t wait_limit_ns() {
 int fault_injection() {
     const char* env = getenv("MOEFP8_FAULT");
     if (env && strcmp(env, "gemm_producer") == 0) return kFaultGemmProducer;
+    if (env && strcmp(env, "ffn_producer") == 0) return kFaultFfnProducer;
+    if (env && strcmp(env, "norm_rows") == 0) return kFaultNormRows;
     return kFaultNone;
 }
 

@@ -317,6 +317,7 @@ struct Stream {
     int ahead;       // rows copied ahead
     int* dev_status;
     uint64_t wait_limit_ns;
+    int fault;       // FaultKind
 };
 struct StreamState {
     uint64_t full[kMaxAhead];
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(kStreamThreads)
     const int t = threadIdx.x, tpr = blockDim.x;
     const int64_t G = gridDim.x;
     auto issue = [&](int64_t row, int slot) {
-        if (row >= rows) return;
+        if (row >= rows || (st.fault == kFaultNormRows && row == blockIdx.x)) return;
         const uint32_t bar = tc::smem_u32(&ss.full[slot]);
         const uint32_t dst = tc::smem_u32(slots + slot * st.slot);
         tc::mbar_arrive_expect_tx(bar, row_bytes(x, row) + row_bytes(dy, row));
@@ -661,6 +662,7 @@ int backward_any(bool vec, const BwdArgs& a, cudaStream_t st) {
         s.ahead = rows_ahead(s.slot, backward_per_sm(a.cols));
         s.dev_status = a.dev_status;
         s.wait_limit_ns = wait_limit_ns();
+        s.fault = fault_injection();
         return vec ? backward_stream<T, X, 8>(a, x_slot, s, st)
                    : backward_stream<T, X, 1>(a, x_slot, s, st);
     }

@@ -80,6 +80,21 @@ __device__ __forceinline__ uint64_t quiesce_ns(uint64_t limit_ns) {
     return limit_ns > 1000000ull ? limit_ns : 1000000ull;
 }
 
+// After an abort, before the stages are used for anything else and before the
+// CTA leaves: waits until the newest load of each stage of a ring has landed.
+// `issued` steps have been loaded, step i into stage i % stages; a step that
+// was not loaded in full never completes, and the wait ends at the limit, in
+// which every copy of it has long landed.
+__device__ __forceinline__ void ring_quiesce(const uint64_t* full, uint32_t stages,
+                                             uint32_t issued, uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer_ns(), limit = quiesce_ns(limit_ns);
+    for (uint32_t i = issued > stages ? issued - stages : 0; i < issued; ++i) {
+        const uint64_t spent = globaltimer_ns() - t0;
+        mbar_quiesce(smem_u32(&full[i % stages]), (i / stages) & 1u, nullptr,
+                     spent < limit ? limit - spent : 0);
+    }
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int x, int y) {
     asm volatile(

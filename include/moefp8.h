@@ -46,11 +46,13 @@
  *     in flight is waited for, TMEM is freed); the context stays usable.
  *     The environment variable MOEFP8_WAIT_LIMIT_NS (read at every call)
  *     sets another limit in nanoseconds (at least 1000).
- *   - Fault injection for tests of that path: MOEFP8_FAULT=gemm_producer
- *     (read at every call) makes the single-CTA grouped GEMM's TMA producer
- *     withhold the loads of its first stage, so that the MMA issuer's wait
- *     on that stage runs out.  Nothing faults or hangs; the call's results
- *     are garbage and dev_status reads MOE_DEV_TIMEOUT.  Unset in normal use.
+ *   - Fault injection for tests of that path: MOEFP8_FAULT (read at every
+ *     call) makes a kernel's TMA producer withhold the loads of its first
+ *     stage, so that the wait on that stage runs out: gemm_producer in the
+ *     single-CTA grouped GEMM, ffn_producer in the dense block's kernels that
+ *     load by TMA, norm_rows in the norm's backward pass that streams rows.
+ *     Nothing faults or hangs; the call's results are garbage and dev_status
+ *     reads MOE_DEV_TIMEOUT.  Unset in normal use.
  */
 #ifndef MOEFP8_H
 #define MOEFP8_H
