@@ -370,7 +370,8 @@ class MoeLayer:
         """The forward pass (fp32-scale recipe) through the stage entry points,
         keeping what backward() needs: the chosen affinities, the permuted FP8
         rows and the expert outputs.  y equals forward()'s bit for bit; x
-        must stay unchanged until backward() has run.
+        must stay unchanged until backward() has run, so y may not be x, unless
+        it goes through a norm and keep is "fp8".
 
         keep: None keeps the expert outputs in fp32 and lets backward()
         recompute gate and up from the FP8 rows (one more W13 GEMM).  "fp8"
@@ -381,6 +382,8 @@ class MoeLayer:
             raise ValueError("the backward pass uses the fp32-scale layer")
         if keep is not None and keep != "fp8":
             raise ValueError("keep must be None or 'fp8'")
+        if y is not None and (self.norm is None or keep is None):
+            _check_not_over(y, x)
         if self.norm is not None:
             x = self.norm.forward_train(x, keep=keep or "full", stream=stream)
         sh, b = self.shape, self._train_buffers()
