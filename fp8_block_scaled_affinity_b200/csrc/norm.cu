@@ -18,7 +18,8 @@
 // barrier nothing else hides.  So rows are streamed: several ahead are copied
 // into shared memory in bulk, which goes on whatever the threads wait for
 // (4096 rows of 7168 kept in 8 bits: 53 us, against 73 us with each row loaded
-// when its turn comes; 47 us since the partial sums leave 16 bytes a lane).
+// when its turn comes; 47 us since the partial sums leave 16 bytes a lane, 48
+// since xh is a difference first).
 // Rows that are no multiple of 16 bytes are copied from the 16-byte boundary
 // before them, and read an element at a time.
 #include <algorithm>
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(1024) layernorm_backward_kernel(const T* __res
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const int c = (t + j * tpr) * E;
-            float xv[E], dv[E], w[E];
+            float xv[E], dv[E], w[E], sc = 1.0f;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 xv[i] = mu;
@@ -175,17 +176,14 @@ __global__ void __launch_bounds__(1024) layernorm_backward_kernel(const T* __res
             }
             if (c < cols) {
                 raw_floats(raw_load<X, E>(x + row * x_pitch + c), xv);
-                if constexpr (sizeof(X) == 1) {
-                    const float sc = x_scales[int64_t(c / kTile) * rows + row];
-#pragma unroll
-                    for (int i = 0; i < E; ++i) xv[i] *= sc;
-                }
+                if constexpr (sizeof(X) == 1) sc = x_scales[int64_t(c / kTile) * rows + row];
                 raw_floats(raw_load<T, E>(dy + row * cols + c), dv);
                 if (weight) raw_floats(raw_load<float, E>(weight + c), w);
             }
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const float h = (xv[i] - mu) * rs, gv = dv[i] * w[i];
+                // (the difference rounded once; columns that are not there: 0)
+                const float h = fmaf(xv[i], sc, -mu) * rs, gv = dv[i] * w[i];
                 xh[j * E + i] = h;
                 g[j * E + i] = gv;
                 s1 += gv;
@@ -337,7 +335,7 @@ struct Turn {
 
 // 16 columns a thread in chunks of E: chunk j starts at column (t + j tpr) E.
 // Bound by the instructions of a row and the walk from one barrier to the next,
-// not by memory: 47 us for 4096 rows of 7168 kept in 8 bits, which read and
+// not by memory: 48 us for 4096 rows of 7168 kept in 8 bits, which read and
 // write 150 MB (23 us).  With 8 columns and twice the threads 60 us, where this
 // form took 53 us (its partial sums were stored 4 bytes a lane then: 6 us).
 template <class T, class X, int E>
@@ -418,28 +416,32 @@ __global__ void __launch_bounds__(kStreamThreads)
         float* const gf = reinterpret_cast<float*>(g);
         const RowView<X, E> xr(x, row, slot, cols);
         const RowView<T, E> dr(dy, row, slot + x_slot, cols);
-        // xh = (x - mu) rstd as x k - mu rstd, k = rstd or a kept tile's scale
-        // times rstd: three roundings of |x| rstd, |mu| rstd and |xh|
-        const float2 off = both(-mu * rs);
+        // xh = (x - mu) rstd, the difference first (of a kept value: code times
+        // scale less mu, rounded once), so that xh's error is relative to xh
+        // however far the row lies from zero
+        const float2 minus_mu = both(-mu);
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const int c = (t + j * tpr) * E;
             float xv[E], dv[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) xv[e] = dv[e] = 0.0f;
-            float k = rs;
+            float sc = 1.0f;
             if (c < cols) {
                 xr.get(c, xv);
                 dr.get(c, dv);
-                if (KEPT) k *= scale_s[par][c / kTile];
+                if (KEPT) sc = scale_s[par][c / kTile];
             }
             // (no columns: dy 0 keeps them out of every sum)
             if constexpr (E == 8) {
 #pragma unroll
-                for (int e = 0; e < E; e += 2)
-                    xh[(j * E + e) / 2] = fma2(make_float2(xv[e], xv[e + 1]), both(k), off);
+                for (int e = 0; e < E; e += 2) {
+                    const float2 x2 = make_float2(xv[e], xv[e + 1]);
+                    xh[(j * E + e) / 2] =
+                        mul2(KEPT ? fma2(x2, both(sc), minus_mu) : add2(x2, minus_mu), both(rs));
+                }
             } else {
-                xf[j] = fmaf(xv[0], k, off.x);
+                xf[j] = fmaf(xv[0], sc, -mu) * rs;
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) gf[j * E + e] = dv[e];
