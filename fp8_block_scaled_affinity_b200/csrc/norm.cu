@@ -607,9 +607,10 @@ int forward_any(bool vec, const void* x, int64_t rows, int cols, const float* w,
         // of 7168: 38.6 us, with 32 41.3 us; bf16 the other way, 104 and 93 us)
         if (chunks > 2048)
             return go(layernorm_forward_kernel<T, 4, 8, false, 1>, n, round_threads(chunks, 8));
-        if (sizeof(T) == 4)
+        if constexpr (sizeof(T) == 4)
             return go(layernorm_forward_kernel<T, 4, 4, false, 2>, n, round_threads(chunks, 4));
-        return go(layernorm_forward_kernel<T, 4, 8, false, 5>, n, round_threads(chunks, 8));
+        else
+            return go(layernorm_forward_kernel<T, 4, 8, false, 5>, n, round_threads(chunks, 8));
     }
     if (cols <= 256) return go(layernorm_forward_kernel<T, 1, 8, true, 1>, warps, 128);
     if (cols <= 4096)
