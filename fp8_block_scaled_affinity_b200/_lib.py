@@ -624,6 +624,16 @@ def _mats(first, *specs):
     return at
 
 
+def _scratch(name, t, dev):
+    """Address of a workspace or status word of any shape (None for None; an
+    address passes): on device `dev`, in one piece."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.get_device() != dev or not t.is_contiguous():
+        _mat(name, t, t.shape)
+    return t.data_ptr()
+
+
 def _current_device() -> int:
     return _get_torch()._C._cuda_getDevice()
 
@@ -666,7 +676,8 @@ def moe_layernorm_forward(x, weight, bias, eps, y, mean=None, rstd=None, dev_sta
         ("weight", weight, (cols,), f32), ("bias", bias, (cols,), f32),
         ("mean", mean, (rows,), f32), ("rstd", rstd, (rows,), f32))
     _check("moe_layernorm_forward", lib().moe_layernorm_forward(
-        px, ty, rows, cols, pw, pb, eps, py, pm, pr, _ptr(dev_status), _stream(stream)))
+        px, ty, rows, cols, pw, pb, eps, py, pm, pr,
+        _scratch("dev_status", dev_status, x.get_device()), _stream(stream)))
 
 
 def moe_layernorm_backward_workspace_size(rows, cols) -> int:
@@ -690,9 +701,10 @@ def moe_layernorm_backward(dy, x, x_scales, weight, mean, rstd, dx, dweight, dbi
         ("dx", dx, (rows, cols), dy.dtype), ("dweight", dweight, (cols,), f32),
         ("dbias", dbias, (cols,), f32))
     nbytes = ws.numel() * ws.element_size() if ws is not None else 0
+    dev = dy.get_device()
     _check("moe_layernorm_backward", lib().moe_layernorm_backward(
-        pdy, ty, px, xt, ps, rows, cols, pw, pm, pr, pdx, pdw, pdb, _ptr(ws), nbytes,
-        _ptr(dev_status), _stream(stream)))
+        pdy, ty, px, xt, ps, rows, cols, pw, pm, pr, pdx, pdw, pdb, _scratch("ws", ws, dev), nbytes,
+        _scratch("dev_status", dev_status, dev), _stream(stream)))
 
 
 def moe_ckpt_row_bytes(cols) -> int:
@@ -706,8 +718,9 @@ def moe_ckpt_pack(x, q, scales, dev_status=None, stream=None):
     rows, cols = x.shape
     px, pq, ps = _mats(("x", x, (rows, cols), x.dtype), ("q", q, (rows, _wide(cols)), _u8()),
                        ("scales", scales, (_tiles(cols), rows), _f32()))
-    _check("moe_ckpt_pack", lib().moe_ckpt_pack(px, ty, rows, cols, pq, ps, _ptr(dev_status),
-                                                _stream(stream)))
+    _check("moe_ckpt_pack", lib().moe_ckpt_pack(
+        px, ty, rows, cols, pq, ps, _scratch("dev_status", dev_status, x.get_device()),
+        _stream(stream)))
 
 
 def moe_ckpt_unpack(q, scales, y, dev_status=None, stream=None):
@@ -716,8 +729,9 @@ def moe_ckpt_unpack(q, scales, y, dev_status=None, stream=None):
     rows, cols = y.shape
     py, pq, ps = _mats(("y", y, (rows, cols), y.dtype), ("q", q, (rows, _wide(cols)), _u8()),
                        ("scales", scales, (_tiles(cols), rows), _f32()))
-    _check("moe_ckpt_unpack", lib().moe_ckpt_unpack(pq, ps, rows, cols, py, ty, _ptr(dev_status),
-                                                    _stream(stream)))
+    _check("moe_ckpt_unpack", lib().moe_ckpt_unpack(
+        pq, ps, rows, cols, py, ty, _scratch("dev_status", dev_status, y.get_device()),
+        _stream(stream)))
 
 
 def moe_grouped_gemm_fp8_ckpt(n_groups, group_offsets, max_rows, a, a_scales, k, w, w_scales, n,
@@ -742,7 +756,8 @@ def moe_swiglu_backward_quant_ckpt(dh, ac_q, ac_scales, rows, inter, rows_total,
     if dh.shape[0] < rows:
         raise ValueError("dh: fewer rows than the call's")
     _check("moe_swiglu_backward_quant_ckpt", lib().moe_swiglu_backward_quant_ckpt(
-        ph, pa, ps, rows, inter, rows_total, pq, pqs, _ptr(dev_status), _stream(stream)))
+        ph, pa, ps, rows, inter, rows_total, pq, pqs,
+        _scratch("dev_status", dev_status, ac_q.get_device()), _stream(stream)))
 
 
 def moe_wgrad_quant_h_ckpt(ac_q, ac_scales, inter, blocks, ht, ht_scales, dev_status=None,
@@ -797,7 +812,8 @@ def moe_ffn_forward(x, w13, w2, h, y, ac=None, ac_scales=None, dev_status=None, 
         ("x", x, (T, d), t), ("w13", w13, (2 * inter, d), t), ("w2", w2, (d, inter), t),
         ("h", h, (T, inter), t), ("y", y, (T, d), t), *kept)
     _check("moe_ffn_forward", lib().moe_ffn_forward(
-        px, p13, p2, ty, T, d, inter, ph, py, pac, at, ps, _ptr(dev_status), _stream(stream)))
+        px, p13, p2, ty, T, d, inter, ph, py, pac, at, ps,
+        _scratch("dev_status", dev_status, x.get_device()), _stream(stream)))
 
 
 def moe_ffn_backward(dy, x, w13, w2, ac, ac_scales, dac, h, dx=None, dw13=None, dw2=None,
@@ -817,4 +833,4 @@ def moe_ffn_backward(dy, x, w13, w2, ac, ac_scales, dac, h, dx=None, dw13=None, 
         *kept)
     _check("moe_ffn_backward", lib().moe_ffn_backward(
         pdy, px, p13, p2, pac, at, ps, ty, T, d, inter, pdac, ph, pdx, pd13, pd2,
-        _ptr(dev_status), _stream(stream)))
+        _scratch("dev_status", dev_status, dy.get_device()), _stream(stream)))
