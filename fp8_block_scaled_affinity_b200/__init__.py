@@ -303,6 +303,14 @@ class MoeLayer:
         self._weights = None
         self._transposed = None
 
+    def _check_normed(self, x):
+        """The norm takes any rows and types; the layer behind it sees addresses."""
+        import torch
+        want = (self.shape.T, self.shape.d)
+        if tuple(x.shape) != want or x.dtype != torch.bfloat16:
+            raise ValueError(f"x must be bf16 {list(want)} for the norm of this layer, got "
+                             f"{x.dtype} {list(x.shape)}")
+
     def weights(self):
         if self._weights is None:
             mk = make_weights if self.scales == "fp32" else make_weights_mx
@@ -314,6 +322,7 @@ class MoeLayer:
         """y = MoE(x) for bf16 x [T, d] on the GPU; returns y (bf16 [T, d])."""
         import torch
         if self.norm is not None:
+            self._check_normed(x)
             x = self.norm.forward(x, stream=stream)
         if y is None:
             y = torch.empty_like(x)
@@ -385,6 +394,7 @@ class MoeLayer:
         if y is not None and (self.norm is None or keep is None):
             _check_not_over(y, x)
         if self.norm is not None:
+            self._check_normed(x)
             x = self.norm.forward_train(x, keep=keep or "full", stream=stream)
         sh, b = self.shape, self._train_buffers()
         b["ac"] = None
