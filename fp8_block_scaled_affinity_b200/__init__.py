@@ -133,14 +133,19 @@ class LayerNorm:
         """dx (dy's type) of the last forward_train(); dy of x's type or fp32.
         dev_status: the word that a wait which ran out is reported on (None: the
         norm's own)."""
-        import torch
         if self._kept is None:
             raise RuntimeError("backward() needs a forward_train() first")
         if dev_status is None:
             if self.dev_status is None:
                 self.dev_status = self._status_word(dy.device)
             dev_status = self.dev_status
-        x, scales, mean, rstd = self._kept
+        return self._backward(self._kept, dy, stream, dev_status)
+
+    def _backward(self, kept, dy, stream, dev_status):
+        """backward() of the forward_train() that kept `kept`: a layer hands in
+        its own, as another layer with the same norm may have run since."""
+        import torch
+        x, scales, mean, rstd = kept
         rows, cols = dy.shape
         dx = torch.empty_like(dy)
         self.dweight = torch.empty((cols,), dtype=torch.float32, device=dy.device)
@@ -208,7 +213,7 @@ class GatedFfn:
             ac, scales = self._hidden(x, 2 * inter), None
         moe_ffn_forward(n, self.w13, self.w2, self._hidden(x, inter), y, ac, scales,
                         self.dev_status, stream)
-        self._kept = (n, ac, scales)
+        self._kept = (n, ac, scales, self.norm and self.norm._kept)
         return y
 
     @_on_stream
@@ -219,7 +224,7 @@ class GatedFfn:
         import torch
         if self._kept is None:
             raise RuntimeError("backward() needs a forward_train() first")
-        n, ac, scales = self._kept
+        n, ac, scales, norm_kept = self._kept
         inter = self.w2.shape[1]
         dx = torch.empty_like(dy)
         dw13 = torch.empty_like(self.w13) if wgrad else None
@@ -227,7 +232,7 @@ class GatedFfn:
         moe_ffn_backward(dy, n, self.w13, self.w2, ac, scales, self._hidden(dy, 2 * inter),
                          self._hidden(dy, inter), dx, dw13, dw2, self.dev_status, stream)
         if self.norm is not None:
-            dx = self.norm.backward(dx, stream=stream, dev_status=self.dev_status)
+            dx = self.norm._backward(norm_kept, dx, stream, self.dev_status)
         return (dx, dw13, dw2) if wgrad else dx
 
     def status(self, stream=None) -> int:
@@ -370,6 +375,7 @@ class MoeLayer:
                 "o": None,  # fp32 [R, d], or (codes, scales) kept in 8 bits
                 "ac": None,  # gate and up kept in 8 bits: (codes, scales)
                 "x": None,
+                "norm": None,  # what its norm kept
             }
         return self._train
 
@@ -429,7 +435,7 @@ class MoeLayer:
         b["o"] = _pack(o, stream) if keep else o
         if update_bias:
             moe_update_bias(sh, self.expert_counts, self.bias, st, stream)
-        b["x"] = x
+        b["x"], b["norm"] = x, self.norm and self.norm._kept
         return y
 
     def _transposed_weights(self, stream=None):
@@ -541,7 +547,7 @@ class MoeLayer:
         mark("dx_combine")
         self.last_dgate, self.last_du = dgate, du
         if self.norm is not None:
-            dx = self.norm.backward(dx, stream=stream, dev_status=self.dev_status)
+            dx = self.norm._backward(b["norm"], dx, stream, self.dev_status)
             mark("norm_backward")
         if not wgrad:
             return dx, d_router_w
