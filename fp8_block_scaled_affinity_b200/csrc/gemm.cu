@@ -288,7 +288,7 @@ __device__ __forceinline__ bool mbar_quiesce(uint32_t bar, uint32_t parity, Shar
                                              int* dev_status) {
     if (mbar_try_wait<kPoll>(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
-    const uint64_t limit = ss->wait_limit;
+    const uint64_t limit = max(ss->wait_limit, uint64_t(1000000));  // a load takes less
     for (uint32_t it = 1;; ++it) {
         if (mbar_try_wait<kPoll>(bar, parity)) return true;
         if ((it & 15) == 0 && globaltimer_ns() - t0 > limit) {
@@ -644,9 +644,10 @@ __device__ __forceinline__ void producer(const GemmParams& p, const CUtensorMap*
             }
         }
     }
-    if (!ok && lane == 0 && rank == 0) {
-        // let loads already in flight land before the CTA leaves (the stage
-        // barriers of a pair are the leader's)
+    if (lane == 0 && rank == 0) {
+        // loads in flight land before the CTA leaves, also when it was another
+        // warp's wait that ran out (the stage barriers of a pair are the
+        // leader's)
         for (int s = 0; s < C::kStages; ++s)
             if ((issued_mask >> s) & 1u)
                 mbar_quiesce(smem_u32(&ss->full[s]), (issued_parity >> s) & 1u, ss, nullptr);
@@ -1284,7 +1285,7 @@ __device__ __forceinline__ void mx_producer(const GemmParams& p, const CUtensorM
             }
         }
     }
-    if (!ok && lane == 0)
+    if (lane == 0)  // (as in producer)
         for (int s = 0; s < C::kStages; ++s)
             if ((issued_mask >> s) & 1u)
                 mbar_quiesce(smem_u32(&ss->full[s]), (issued_parity >> s) & 1u, ss, nullptr);
@@ -1754,7 +1755,7 @@ __device__ __forceinline__ void wg_producer(const WgParams& p, const CUtensorMap
             }
         }
     }
-    if (!ok && lane == 0)
+    if (lane == 0)  // (as in producer)
         for (int s = 0; s < C::kStages; ++s)
             if ((issued_mask >> s) & 1u)
                 mbar_quiesce(smem_u32(&ss->full[s]), (issued_parity >> s) & 1u, ss, nullptr);
