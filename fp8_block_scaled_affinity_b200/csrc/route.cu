@@ -116,6 +116,7 @@ __device__ __forceinline__ float warp_max(float v) {
 // memory (d * 2 bytes; the launch provides kSliceWarps of them) and the
 // second reads it from there; otherwise the second pass reads the row again.
 constexpr int kSliceWarps = 4;
+constexpr int kMaxExperts = 1024;          // of a shape
 constexpr int kSliceStageMax = 32 * 1024;  // largest row staged per warp (d <= 16384)
 __global__ void __launch_bounds__(kSliceWarps * 32) route_slice_kernel(
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ E, int T, int N, int d,
@@ -1143,7 +1144,7 @@ int validate_shape(const MoeShape* s) {
     if (!s) return MOE_ERR_NULL;
     if (s->T < 0 || s->d <= 0 || s->d % 128 || s->inter <= 0 || s->inter % 128)
         return MOE_ERR_SHAPE;
-    if (s->n_routed < 1 || s->n_routed > 1024) return MOE_ERR_SHAPE;
+    if (s->n_routed < 1 || s->n_routed > kMaxExperts) return MOE_ERR_SHAPE;
     if (s->n_groups < 1 || s->n_groups > 32 || s->n_routed % s->n_groups) return MOE_ERR_ROUTE;
     if (s->topk_groups < 1 || s->topk_groups > s->n_groups) return MOE_ERR_ROUTE;
     if (s->topk < 1 || s->topk > 32) return MOE_ERR_ROUTE;
@@ -1250,10 +1251,12 @@ extern "C" MOE_API int moe_route_scores(const MoeShape* shape, const uint16_t* x
     const double nmargin = 4.0 * (d + 64) * 0x1p-53 + 0x1p-50;
     const int staged = 2 * d <= kSliceStageMax;
     const size_t slice_smem = staged ? size_t(kSliceWarps) * 2 * d : 0;
+    // (limits for any shape, not for this call's alone: they are the device's,
+    // and another thread may be between its own and its launch)
     if (slice_smem > 48 * 1024 &&
         cudaFuncSetAttribute(route_slice_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(slice_smem)) != cudaSuccess)
-        return MOE_ERR_CUDA;
+                             kSliceWarps * kSliceStageMax) != cudaSuccess)
+        return cuda_failed();
     route_slice_kernel<<<(T + N + kSliceWarps - 1) / kSliceWarps, kSliceWarps * 32, slice_smem,
                          st>>>(x, router_w, T, N, d, nmargin, staged, w.xp, w.ep, w.rsc, w.rex,
                                w.r1, w.l2, w.vmax, w.vmin, w.lb, w.list_count, w.pair_count,
@@ -1289,8 +1292,9 @@ extern "C" MOE_API int moe_route_scores(const MoeShape* shape, const uint16_t* x
     const size_t csmem = sizeof(float) * 3 * size_t(cert_pitch(N)) * kCertWarps;
     if (csmem > 48 * 1024 &&
         cudaFuncSetAttribute(route_certify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(csmem)) != cudaSuccess)
-        return MOE_ERR_CUDA;
+                             int(sizeof(float)) * 3 * cert_pitch(kMaxExperts) * kCertWarps) !=
+            cudaSuccess)
+        return cuda_failed();
     route_certify_kernel<<<(T + kCertWarps - 1) / kCertWarps, kCertWarps * 32, csmem, st>>>(
         w.acc, w.rsc, w.rex, w.r1, w.l2, w.vmax, w.lb, bias, logit_offset, T, N, shape->n_groups,
         shape->topk_groups, K, gamma64, w.cand, w.cert, w.u_exact, w.list, w.list_count,
@@ -1325,8 +1329,8 @@ extern "C" MOE_API int moe_route_scores(const MoeShape* shape, const uint16_t* x
     const size_t smem = sizeof(float) * size_t(N) * (1 + 2 * kSelWarps);
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(route_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(smem)) != cudaSuccess)
-        return MOE_ERR_CUDA;
+                             int(sizeof(float)) * kMaxExperts * (1 + 2 * kSelWarps)) != cudaSuccess)
+        return cuda_failed();
     route_select_kernel<<<(T + kSelWarps - 1) / kSelWarps, kSelWarps * 32, smem, st>>>(
         w.uhat, w.cert, w.cand, w.u_exact, T, N, shape->n_groups, shape->topk_groups, K, bias,
         logit_offset, topk_idx, topk_gate, topk_score, expert_counts, dev_status, w.check);
