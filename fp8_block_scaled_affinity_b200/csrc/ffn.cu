@@ -276,8 +276,9 @@ __device__ __forceinline__ void put32(const float (&v)[32], char* park, int& box
     }
 }
 
-// sigmoid from the fast exponential and reciprocal (about 1e-6 relative;
-// e^-a = inf gives 0)
+// sigmoid from the fast exponential and reciprocal (about 1e-6 relative, where
+// what follows is rounded to 16 bits: 5e-4 in fp16, 4e-3 in bf16; e^-a = inf
+// gives 0)
 __device__ __forceinline__ float sigmoid_fast(float a) {
     return __fdividef(1.0f, 1.0f + __expf(-a));
 }
