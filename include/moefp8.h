@@ -817,7 +817,7 @@ MOE_API int moe_layernorm_backward(const void* dy, int type, const void* x, int 
  *   as ac_q (uint8 [rows, 2 inter]) and ac_scales (fp32 [2 inter / 128,
  *   rows_total]): the bits of that call on the unpacked values, except that a
  *   tile of [da | dc] whose amax is between 0 and 2^-119 is scaled as one of
- *   2^-119.
+ *   2^-119, and sigmoid(a) is 0 where it is subnormal (a below -87.3).
  * moe_wgrad_quant_h_ckpt, moe_wgrad_quant_dac_ckpt: moe_wgrad_quant_h and
  *   _dac with [a | c] kept so; rows_total is the scales' row length.
  * moe_gate_backward_ckpt: moe_gate_backward with the expert outputs kept as
